@@ -16,7 +16,7 @@
 
 #include <cstdarg>
 #include <string>
-#include <unordered_map>
+#include <type_traits>
 #include <vector>
 
 #include "../../include/uf_layers.h"
@@ -388,21 +388,22 @@ PyObject* gated_bwd(PyObject* const* a) {
   return out.dict;
 }
 
-// The optimizer's tensors, checked once; the plan holds references to them.
-struct AdamPlan {
-  std::vector<Tensor> held;
+// The optimizer's tensors as a step finds them.  Nothing of them is kept between steps: the storage
+// under a tensor may be replaced at any time (p.data = ..., set_, resize_, a state moved to the
+// host and back), and so may an entry of the lists.
+struct AdamTensors {
   std::vector<void*> p, m, v, copy;
   std::vector<float*> ms, vs;
-  std::vector<int64_t> sizes;
   std::vector<const void*> g;
+  std::vector<int64_t> sizes;
   c10::Device dev{c10::kCPU};
-  at::ScalarType ptype = at::kFloat, stype = at::kFloat;
+  at::ScalarType ptype = at::kFloat, stype = at::kFloat, gtype = at::kFloat;
 };
 constexpr int64_t kStateBlock = 256;  // elements that share a scale in 8-bit states
 
-// Calls f(i, tensor) for a list of contiguous CUDA tensors of one type on the plan's device.
+// Calls f(i, tensor) for a list of contiguous CUDA tensors of one type on dev.
 template <typename F>
-void each(const AdamPlan& plan, const char* name, PyObject* list, Types types, int64_t n, const std::vector<int64_t>* numels,
+void each(const c10::Device& dev, const char* name, PyObject* list, Types types, int64_t n, const std::vector<int64_t>* numels,
           at::ScalarType* type, F&& f) {
   PyObject* seq = PySequence_Fast(list, name);
   if (!seq) throw Raised{};
@@ -418,11 +419,11 @@ void each(const AdamPlan& plan, const char* name, PyObject* list, Types types, i
       if (!ok || !want.has(THPVariable_Unpack(items[i]).scalar_type()) || !THPVariable_Unpack(items[i]).is_cuda())
         raise(PyExc_TypeError, "%s[%lld] must be a CUDA tensor of %s", name, static_cast<long long>(i), want.names().c_str());
       const Tensor& t = THPVariable_Unpack(items[i]);
-      if (t.device() != plan.dev || !t.is_contiguous() || (numels && t.numel() != (*numels)[i])) {
+      if (t.device() != dev || !t.is_contiguous() || (numels && t.numel() != (*numels)[i])) {
         if (numels)
           raise(PyExc_ValueError, "%s[%lld] must be contiguous, on %s and have %lld elements", name, static_cast<long long>(i),
-                plan.dev.str().c_str(), static_cast<long long>((*numels)[i]));
-        raise(PyExc_ValueError, "%s[%lld] must be contiguous and on %s", name, static_cast<long long>(i), plan.dev.str().c_str());
+                dev.str().c_str(), static_cast<long long>((*numels)[i]));
+        raise(PyExc_ValueError, "%s[%lld] must be contiguous and on %s", name, static_cast<long long>(i), dev.str().c_str());
       }
       f(i, t);
     }
@@ -433,89 +434,85 @@ void each(const AdamPlan& plan, const char* name, PyObject* list, Types types, i
   Py_DECREF(seq);
 }
 
-void free_plan(PyObject* capsule) { delete static_cast<AdamPlan*>(PyCapsule_GetPointer(capsule, "uf_adam_plan")); }
-
-// params, m, v, m_scale, v_scale, copies -> a plan
-PyObject* adamw_plan(PyObject* const* a) {
-  auto plan = std::make_unique<AdamPlan>();
+// params, m, v, m_scale, v_scale, copies
+AdamTensors adam_tensors(PyObject* const* a) {
+  AdamTensors q;
   const Py_ssize_t n = PySequence_Size(a[0]);
   if (n < 0) throw Raised{};
   if (n > 0) {
     PyObject* first = PySequence_GetItem(a[0], 0);
-    if (first && THPVariable_Check(first)) plan->dev = THPVariable_Unpack(first).device();
+    if (first && THPVariable_Check(first)) q.dev = THPVariable_Unpack(first).device();
     Py_XDECREF(first);
   }
-  AdamPlan& q = *plan;
-  auto keep = [&](std::vector<void*>& to) {
+  auto keep = [&](auto& to) {
+    to.reserve(static_cast<size_t>(n));
     return [&](int64_t, const Tensor& t) {
-      q.held.push_back(t);
-      to.push_back(t.data_ptr());
+      to.push_back(static_cast<typename std::decay_t<decltype(to)>::value_type>(t.data_ptr()));
     };
   };
-  each(q, "params", a[0], kFloats, n, nullptr, &q.ptype, [&](int64_t, const Tensor& t) {
-    q.held.push_back(t);
+  q.p.reserve(static_cast<size_t>(n));
+  q.sizes.reserve(static_cast<size_t>(n));
+  each(q.dev, "params", a[0], kFloats, n, nullptr, &q.ptype, [&](int64_t, const Tensor& t) {
     q.p.push_back(t.data_ptr());
     q.sizes.push_back(t.numel());
   });
   const Types states{at::kFloat, at::kFloat8_e4m3fn};
-  each(q, "m", a[1], states, n, &q.sizes, &q.stype, keep(q.m));
+  each(q.dev, "m", a[1], states, n, &q.sizes, &q.stype, keep(q.m));
   at::ScalarType v_type = q.stype;
-  each(q, "v", a[2], Types{q.stype, q.stype}, n, &q.sizes, &v_type, keep(q.v));
+  each(q.dev, "v", a[2], Types{q.stype, q.stype}, n, &q.sizes, &v_type, keep(q.v));
   const bool e8 = n > 0 && q.stype == at::kFloat8_e4m3fn;
   if (e8 != given(a[3]) || e8 != given(a[4])) raise(PyExc_ValueError, "m_scale and v_scale go with 8-bit states");
   if (e8) {
     std::vector<int64_t> blocks;
+    blocks.reserve(static_cast<size_t>(n));
     for (int64_t s : q.sizes) blocks.push_back((s + kStateBlock - 1) / kStateBlock);
     at::ScalarType f = at::kFloat;
-    auto scales = [&](std::vector<float*>& to) {
-      return [&](int64_t, const Tensor& t) {
-        q.held.push_back(t);
-        to.push_back(static_cast<float*>(t.data_ptr()));
-      };
-    };
-    each(q, "m_scale", a[3], kF32, n, &blocks, &f, scales(q.ms));
-    each(q, "v_scale", a[4], kF32, n, &blocks, &f, scales(q.vs));
+    each(q.dev, "m_scale", a[3], kF32, n, &blocks, &f, keep(q.ms));
+    each(q.dev, "v_scale", a[4], kF32, n, &blocks, &f, keep(q.vs));
   }
   if (given(a[5])) {
     if (q.ptype != at::kFloat) raise(PyExc_ValueError, "copies go with fp32 parameters");
     at::ScalarType b = at::kBFloat16;
-    each(q, "copies", a[5], kBf16, n, &q.sizes, &b, keep(q.copy));
+    each(q.dev, "copies", a[5], kBf16, n, &q.sizes, &b, keep(q.copy));
   }
-  q.g.resize(static_cast<size_t>(n));
-  PyObject* capsule = PyCapsule_New(plan.get(), "uf_adam_plan", free_plan);
-  if (!capsule) throw Raised{};
-  plan.release();
-  return capsule;
+  return q;
 }
 
-// plan, grads, lr (float or tensor), betas[0], betas[1], eps, weight_decay, step, step_dev, seed, grad_scale, stream
+// params, m, v, m_scale, v_scale, copies: checks them
+PyObject* adamw_check(PyObject* const* a) {
+  adam_tensors(a);
+  Py_RETURN_NONE;
+}
+
+// params, m, v, m_scale, v_scale, copies, grads, lr (float or tensor), betas[0], betas[1], eps, weight_decay,
+// step, step_dev, seed, grad_scale, stream
 PyObject* adamw_step(PyObject* const* a) {
-  auto* q = static_cast<AdamPlan*>(PyCapsule_GetPointer(a[0], "uf_adam_plan"));
-  if (!q) throw Raised{};
-  const int64_t n = static_cast<int64_t>(q->sizes.size());
-  at::ScalarType gtype = at::kFloat;
-  each(*q, "grads", a[1], kFloats, n, &q->sizes, &gtype, [&](int64_t i, const Tensor& t) { q->g[i] = t.data_ptr(); });
+  AdamTensors q = adam_tensors(a);
+  a += 6;
+  const int64_t n = static_cast<int64_t>(q.sizes.size());
+  q.g.reserve(static_cast<size_t>(n));
+  each(q.dev, "grads", a[0], kFloats, n, &q.sizes, &q.gtype, [&](int64_t, const Tensor& t) { q.g.push_back(t.data_ptr()); });
   if (n == 0) Py_RETURN_NONE;
   auto scalar = [&](const char* name, PyObject* o, at::ScalarType t) -> void* {
     if (!given(o)) return nullptr;
-    if (!THPVariable_Check(o) || THPVariable_Unpack(o).scalar_type() != t || THPVariable_Unpack(o).device() != q->dev ||
+    if (!THPVariable_Check(o) || THPVariable_Unpack(o).scalar_type() != t || THPVariable_Unpack(o).device() != q.dev ||
         THPVariable_Unpack(o).numel() != 1)
       raise(PyExc_TypeError, "%s must be a one-element %s tensor on %s", name, t == at::kFloat ? "float32" : "int64",
-            q->dev.str().c_str());
+            q.dev.str().c_str());
     return THPVariable_Unpack(o).data_ptr();
   };
-  const bool lr_tensor = THPVariable_Check(a[2]);
-  const auto* lr_dev = static_cast<const float*>(lr_tensor ? scalar("lr", a[2], at::kFloat) : nullptr);
-  const float lr = lr_tensor ? 0.f : static_cast<float>(number(a[2]));
-  const auto* step_dev = static_cast<const int64_t*>(scalar("step_dev", a[8], at::kLong));
-  const auto* gs = static_cast<const float*>(scalar("grad_scale", a[10], at::kFloat));
-  const On on(q->dev, a[11]);
-  check(api.adamw_step(static_cast<int>(n), q->p.data(), q->g.data(), q->m.data(), q->v.data(),
-                       q->ms.empty() ? nullptr : q->ms.data(), q->vs.empty() ? nullptr : q->vs.data(),
-                       q->copy.empty() ? nullptr : q->copy.data(), q->sizes.data(), type_of(q->ptype), type_of(gtype),
-                       type_of(q->stype), lr, lr_dev, number(a[3]), number(a[4]),
-                       static_cast<float>(number(a[5])), static_cast<float>(number(a[6])), integer(a[7]), step_dev,
-                       static_cast<uint32_t>(integer(a[9])), gs, on.stream),
+  const bool lr_tensor = THPVariable_Check(a[1]);
+  const auto* lr_dev = static_cast<const float*>(lr_tensor ? scalar("lr", a[1], at::kFloat) : nullptr);
+  const float lr = lr_tensor ? 0.f : static_cast<float>(number(a[1]));
+  const auto* step_dev = static_cast<const int64_t*>(scalar("step_dev", a[7], at::kLong));
+  const auto* gs = static_cast<const float*>(scalar("grad_scale", a[9], at::kFloat));
+  const On on(q.dev, a[10]);
+  check(api.adamw_step(static_cast<int>(n), q.p.data(), q.g.data(), q.m.data(), q.v.data(),
+                       q.ms.empty() ? nullptr : q.ms.data(), q.vs.empty() ? nullptr : q.vs.data(),
+                       q.copy.empty() ? nullptr : q.copy.data(), q.sizes.data(), type_of(q.ptype), type_of(q.gtype),
+                       type_of(q.stype), lr, lr_dev, number(a[2]), number(a[3]),
+                       static_cast<float>(number(a[4])), static_cast<float>(number(a[5])), integer(a[6]), step_dev,
+                       static_cast<uint32_t>(integer(a[8])), gs, on.stream),
         "uf_adamw_step");
   Py_RETURN_NONE;
 }
@@ -575,8 +572,8 @@ PyMethodDef methods[] = {method<bind, 2, false>("bind"),
                          method<linear_bwd, 11>("linear_bwd"),
                          method<gated_fwd, 7>("gated_fwd"),
                          method<gated_bwd, 10>("gated_bwd"),
-                         method<adamw_plan, 6>("adamw_plan"),
-                         method<adamw_step, 12>("adamw_step"),
+                         method<adamw_check, 6>("adamw_check"),
+                         method<adamw_step, 17>("adamw_step"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layers_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -149,13 +149,18 @@ class AdamW:
     states in the same order, fp32, or float8_e4m3fn codes of m and sqrt(v) with fp32 scales
     ``m_scale`` / ``v_scale`` for blocks of 256 elements; ``new_states`` makes them.  copies:
     bf16 tensors that receive the new fp32 parameters (the operands of the next forward).
-    step: steps already taken."""
+    step: steps already taken.
+
+    The lists are the attributes ``params``, ``m``, ``v``, ``m_scale``, ``v_scale`` and ``copies``.
+    Every step reads and checks them anew, so entries may be replaced between steps (a loaded
+    checkpoint) and tensors may get other storage (``p.data = ...``, a state moved away and back);
+    a captured step keeps the addresses that it was captured with."""
 
     def __init__(self, params, m, v, m_scale=None, v_scale=None, copies=None, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.01, step=0):
         self.params, self.m, self.v, self.m_scale, self.v_scale, self.copies = params, m, v, m_scale, v_scale, copies
         self.betas, self.eps, self.weight_decay, self.t = betas, eps, weight_decay, step
-        self._plan = _native.adamw_plan(params, m, v, m_scale, v_scale, copies)
+        _native.adamw_check(params, m, v, m_scale, v_scale, copies)
 
     @staticmethod
     def new_states(params, bits=32):
@@ -178,6 +183,6 @@ class AdamW:
         t = self.t + 1
         if seed is None:
             seed = 0 if step_dev is not None else t
-        _native.adamw_step(self._plan, grads, lr, *self.betas, self.eps, self.weight_decay, t, step_dev, seed & 0xFFFFFFFF,
-                           grad_scale, stream)
+        _native.adamw_step(self.params, self.m, self.v, self.m_scale, self.v_scale, self.copies, grads, lr, *self.betas,
+                           self.eps, self.weight_decay, t, step_dev, seed & 0xFFFFFFFF, grad_scale, stream)
         self.t = t

@@ -1,0 +1,73 @@
+"""The head's operators and the optimizer where they can go wrong beside the ordinary sizes: replaced
+storage, the ends of the formats' ranges, sides of a limit, calls from threads and other streams.
+Tolerances as in ``test_layers_gpu``."""
+import pytest
+
+torch = pytest.importorskip("torch")
+from test_layers_gpu import E4, L, rand  # noqa: F401,E402
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------------------------- AdamW
+
+def raw(t):
+    return t.view(torch.uint8) if t.dtype == E4 else t
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_follows_tensors_whose_storage_is_replaced(L, bits):
+    """The step writes where its tensors are now, and not where they were."""
+    p, g = [rand(1, 1000), rand(2, 70000)], [rand(3, 1000), rand(4, 70000)]
+    copies = [t.bfloat16() for t in p]
+    opt = L.AdamW(p, *L.AdamW.new_states(p, bits), copies=copies)
+    opt.step(g, lr=1e-2)
+    twin_p = [t.clone() for t in p]
+    lists = [opt.m, opt.v] + ([opt.m_scale, opt.v_scale] if bits == 8 else [])
+    twin_s = [[raw(t).clone().view(t.dtype) for t in ts] for ts in lists]
+    twin = L.AdamW(twin_p, *twin_s, copies=[t.clone() for t in copies], step=1)
+    everything = [t for ts in [p, copies] + lists for t in ts]
+    old = [raw(t.data) for t in everything]
+    before = [t.clone() for t in old]
+    for t in everything:
+        t.data = raw(t.data).clone().view(t.dtype)
+    opt.step(g, lr=1e-2)
+    twin.step(g, lr=1e-2)
+    now = [t for ts in [twin.params, twin.copies] + twin_s for t in ts]
+    assert all(torch.equal(raw(a), raw(b)) for a, b in zip(everything, now))
+    assert all(torch.equal(a, b) for a, b in zip(old, before))
+    assert not torch.equal(p[0], before[0])
+
+
+def test_adamw_follows_replaced_entries_of_its_lists(L):
+    p, g = [rand(1, 500)], [rand(2, 500)]
+    opt = L.AdamW(p, *L.AdamW.new_states(p))
+    opt.step(g, lr=1e-2)
+    m, v, new = opt.m[0].clone(), opt.v[0].clone(), rand(3, 500)
+    opt.params[0], opt.m[0], opt.v[0] = new.clone(), m.clone(), v.clone()  # a loaded checkpoint
+    opt.step(g, lr=1e-2)
+    twin = L.AdamW([new], [m], [v], step=1)
+    twin.step(g, lr=1e-2)
+    assert torch.equal(opt.params[0], new) and torch.equal(opt.m[0], m) and torch.equal(opt.v[0], v)
+
+
+def test_adamw_refuses_tensors_that_no_longer_fit(L):
+    p, g = [rand(1, 500)], [rand(2, 500)]
+    opt = L.AdamW(p, *L.AdamW.new_states(p))
+    p[0].data = rand(3, 400)
+    with pytest.raises(ValueError, match="400 elements"):
+        opt.step(g, lr=1e-2)
+    p[0].data = rand(3, 1000)[::2]
+    with pytest.raises(ValueError, match="contiguous"):
+        opt.step(g, lr=1e-2)
+    p[0].data = rand(3, 500)
+    opt.m[0] = opt.m[0].bfloat16()
+    with pytest.raises(TypeError, match=r"m\[0\]"):
+        opt.step(g, lr=1e-2)
+    opt.m[0] = torch.zeros(500)
+    with pytest.raises(TypeError, match=r"m\[0\]"):
+        opt.step(g, lr=1e-2)
+    opt.params.append(rand(4, 3))
+    with pytest.raises(ValueError, match="hold 2 tensors"):
+        opt.step(g, lr=1e-2)
+    assert opt.t == 0
