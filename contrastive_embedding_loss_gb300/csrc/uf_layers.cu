@@ -5,9 +5,13 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <initializer_list>
+#include <memory>
+#include <new>
+#include <utility>
 
 #include "../../include/uf_layers.h"
 #include "layers.h"
@@ -45,6 +49,51 @@ bool disjoint(std::initializer_list<Range> written, std::initializer_list<Range>
       if (overlap(*i, *j)) return false;
     for (const Range& r : read)
       if (overlap(*i, r)) return false;
+  }
+  return true;
+}
+
+// The ranges of a long list of buffers, sorted by their start.  Lists come as a few ascending runs (one
+// of parameters, one of states, ...), so runs are merged as they are found: the 960 ranges of 160
+// tensors take 6 us of a call, 17 in random order.
+struct Ranges {
+  std::unique_ptr<Range[]> own;
+  Range* r = nullptr;
+  int n = 0;
+  explicit Ranges(int64_t most) : own(new (std::nothrow) Range[2 * static_cast<size_t>(most)]), r(own.get()), most_(most) {}
+  void add(const Range& x) {
+    if (x.lo < x.hi) r[n++] = x;
+  }
+  void sort() {
+    const auto before = [](const Range& x, const Range& y) { return x.lo < y.lo; };
+    Range* to = r == own.get() ? r + most_ : own.get();
+    for (int runs = 2; runs > 1; std::swap(r, to)) {
+      runs = 0;
+      for (Range* i = r; i < r + n; ++runs) {
+        Range* mid = std::is_sorted_until(i, r + n, before);
+        Range* end = std::is_sorted_until(mid, r + n, before);
+        std::merge(i, mid, mid, end, to + (i - r), before);
+        i = end;
+      }
+    }
+  }
+
+ private:
+  int64_t most_;
+};
+// disjoint() of long lists, which it sorts.
+bool disjoint(Ranges& written, Ranges& read) {
+  written.sort();
+  read.sort();
+  for (int i = 1; i < written.n; ++i)
+    if (written.r[i].lo < written.r[i - 1].hi) return false;
+  for (int i = 0, j = 0; i < written.n && j < read.n;) {
+    const Range &w = written.r[i], &x = read.r[j];
+    if (w.lo < x.hi && x.lo < w.hi) return false;
+    if (x.hi <= w.lo)
+      ++j;
+    else
+      ++i;
   }
   return true;
 }
@@ -501,6 +550,9 @@ uf_status_t uf_adamw_step(int n, void* const* p, const void* const* g, void* con
     return UF_INVALID_ARGUMENT;
   if (!aligned(lr_dev, 4) || !aligned(step_dev, 8) || !aligned(grad_scale_dev, 4)) return UF_INVALID_ARGUMENT;
   const int pe = elem_size(param_type), ge = elem_size(grad_type), se = elem_size(state_type);
+  if (n == 0) return UF_OK;
+  Ranges written(6 * static_cast<int64_t>(n)), read(static_cast<int64_t>(n) + 3);
+  if (!written.r || !read.r) return UF_CUDA_ERROR;
   for (int i = 0; i < n; ++i) {
     if (sizes[i] < 0) return UF_INVALID_ARGUMENT;
     if (sizes[i] == 0) continue;
@@ -508,14 +560,19 @@ uf_status_t uf_adamw_step(int n, void* const* p, const void* const* g, void* con
     if (!aligned(p[i], pe) || !aligned(g[i], ge) || !aligned(m[i], se) || !aligned(v[i], se)) return UF_INVALID_ARGUMENT;
     if (e8 && (!aligned(m_scale[i], 4) || !aligned(v_scale[i], 4))) return UF_INVALID_ARGUMENT;
     if (copy && !aligned(copy[i], 2)) return UF_INVALID_ARGUMENT;
-    const int64_t blocks = (sizes[i] + kAdamBlock - 1) / kAdamBlock;
-    if (!disjoint({vec(p[i], sizes[i], pe), vec(m[i], sizes[i], se), vec(v[i], sizes[i], se),
-                   vec(e8 ? m_scale[i] : nullptr, blocks, 4), vec(e8 ? v_scale[i] : nullptr, blocks, 4),
-                   vec(copy ? copy[i] : nullptr, sizes[i], 2)},
-                  {vec(g[i], sizes[i], ge), vec(lr_dev, 1, 4), vec(step_dev, 1, 8), vec(grad_scale_dev, 1, 4)}))
-      return UF_INVALID_ARGUMENT;
+    written.add(vec(p[i], sizes[i], pe));
+    read.add(vec(g[i], sizes[i], ge));
   }
-  if (n == 0) return UF_OK;
+  // list by list: each is an ascending run of addresses as a rule
+  for (int i = 0; i < n; ++i) written.add(vec(m[i], sizes[i], se));
+  for (int i = 0; i < n; ++i) written.add(vec(v[i], sizes[i], se));
+  for (int i = 0; copy && i < n; ++i) written.add(vec(copy[i], sizes[i], 2));
+  for (auto* scale : {m_scale, v_scale})
+    for (int i = 0; e8 && i < n; ++i) written.add(vec(scale[i], (sizes[i] + kAdamBlock - 1) / kAdamBlock, 4));
+  read.add(vec(lr_dev, 1, 4));
+  read.add(vec(step_dev, 1, 8));
+  read.add(vec(grad_scale_dev, 1, 4));
+  if (!disjoint(written, read)) return UF_INVALID_ARGUMENT;
   const uf_status_t st = ready();
   if (st != UF_OK) return st;
   AdamScalars sc{};

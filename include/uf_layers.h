@@ -132,7 +132,9 @@ UF_API uf_status_t uf_gated_bwd(const void* dh, int64_t lddh, const void* x, int
  * One AdamW step over n tensors (decoupled weight decay), in place.  With g = grad * grad_scale:
  *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
  *   p -= lr (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay p).
- * Host arrays of n device pointers each; they are read before the call returns.
+ * Host arrays of n device pointers each; they are read before the call returns.  What is written
+ * (all but the gradients) may not overlap across tensors either: a parameter listed twice is refused.
+ * Tensors may share a gradient.
  *   p            parameters, param_type UF_F32 or UF_BF16 (bf16: rounded stochastically).
  *   g            gradients, grad_type UF_F32 or UF_BF16.
  *   m, v         state_type UF_F32: fp32.  UF_E4M3: codes of m and of sqrt(v), with fp32 scales

@@ -71,3 +71,31 @@ def test_adamw_refuses_tensors_that_no_longer_fit(L):
     with pytest.raises(ValueError, match="hold 2 tensors"):
         opt.step(g, lr=1e-2)
     assert opt.t == 0
+
+
+def test_adamw_refuses_buffers_shared_by_two_tensors(L):
+    """Two warps of a launch would read and write the same elements.  Gradients may be shared."""
+    from contrastive_embedding_loss_gb300.binding import UfError
+
+    p, q, g = rand(1, 500), rand(2, 500), rand(3, 500)
+
+    def step(params, grads, m=None, v=None):
+        new_m, new_v = L.AdamW.new_states(params)
+        L.AdamW(params, m or new_m, v or new_v).step(grads, lr=1e-2)
+
+    for bad in ([p, p], [p, q, p], [p, p[100:200]]):
+        start = p.clone()
+        with pytest.raises(UfError, match="invalid-argument"):
+            step(bad, [g[:t.numel()] for t in bad])
+        assert torch.equal(p, start)
+    m = [rand(4, 500)] * 2
+    with pytest.raises(UfError, match="invalid-argument"):
+        step([p, q], [g, g], m=m)
+    with pytest.raises(UfError, match="invalid-argument"):
+        step([p, q], [g, p])
+    want_p, want_q = p.clone(), q.clone()
+    step([want_p], [g])
+    step([want_q], [g])
+    flat = torch.cat([q, p])  # neighbours in one buffer, in falling order, with one gradient
+    step([flat[500:], flat[:500]], [g, g])
+    assert torch.equal(flat[500:], want_p) and torch.equal(flat[:500], want_q)
