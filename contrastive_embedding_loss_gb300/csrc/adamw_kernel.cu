@@ -263,10 +263,13 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < 8; ++j) rnd[j] = hash32(static_cast<uint32_t>(i0 + j) + key);
     }
-    if constexpr (sizeof(PT) == 2) {  // 16 random bits below the bf16's own, then cut
+    if constexpr (sizeof(PT) == 2) {
+      // 16 random bits below the bf16's own, then cut (a NaN's would carry into its sign)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        p[j] = __uint_as_float((__float_as_uint(p[j]) + (hash32(rnd[j] ^ 0x9E3779B9u) & 0xFFFFu)) & 0xFFFF0000u);
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t up = __float_as_uint(p[j]) + (hash32(rnd[j] ^ 0x9E3779B9u) & 0xFFFFu);
+        if (!isnan(p[j])) p[j] = __uint_as_float(up & 0xFFFF0000u);
+      }
     }
     if (wide) {
       store8(pp, p);

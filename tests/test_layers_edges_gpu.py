@@ -4,7 +4,7 @@ Tolerances as in ``test_layers_gpu``."""
 import pytest
 
 torch = pytest.importorskip("torch")
-from test_layers_gpu import E4, L, rand  # noqa: F401,E402
+from test_layers_gpu import BF, E4, F32, L, rand  # noqa: F401,E402
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +99,14 @@ def test_adamw_refuses_buffers_shared_by_two_tensors(L):
     flat = torch.cat([q, p])  # neighbours in one buffer, in falling order, with one gradient
     step([flat[500:], flat[:500]], [g, g])
     assert torch.equal(flat[500:], want_p) and torch.equal(flat[:500], want_q)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("gt", [F32, BF])
+def test_adamw_bf16_parameters_keep_a_nan(L, bits, gt):
+    """Rounding at random adds 16 bits below bf16's own: a NaN stays one."""
+    for bad in (float("nan"), float("inf")):
+        p, g = [rand(1, 1000, dtype=BF)], rand(2, 1000, dtype=gt)
+        g[300] = bad
+        L.AdamW(p, *L.AdamW.new_states(p, bits)).step([g], lr=1e-3)
+        assert p[0][300].isnan() and int(p[0].isfinite().sum()) == 999
