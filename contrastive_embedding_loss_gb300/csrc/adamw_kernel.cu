@@ -15,7 +15,8 @@
 // while codes of r are 6 to 12 % apart, so rounding to nearest would freeze v: the codes are
 // rounded at random, up with the probability that makes m and v (r squared, not r: E[r^2] exceeds
 // E[r]^2, which would inflate v at every step) unbiased.  A nonzero v never rounds to code 0,
-// which would make its next update m / eps.
+// which would make its next update m / eps.  A block in which v overflows keeps an infinite scale, and
+// every code of it becomes 126: from then on its elements take no step, as sqrt(v) = inf has it.
 #include "layers.cuh"
 
 namespace ufc {
@@ -94,14 +95,17 @@ struct Step {
 };
 
 // sqrt(v) to the nearest: an approximate reciprocal root y, r = v y, and one step of the coupled
-// Newton iteration (Markstein), r + (v - r^2) y / 2.  v below 2^-126 counts as 0.
+// Newton iteration (Markstein), r + (v - r^2) y / 2.  v below 2^-126 counts as 0.  Of an infinite v that
+// is NaN (inf 0); v 2^-70, which is below the root of every finite v, is infinite there, and a maximum
+// takes the other operand of a NaN.  (A NaN v makes both NaN.)
 __device__ __forceinline__ float2 sqrt2(float2 v) {
   float2 y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(v.x, 1.18e-38f)));
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(v.y, 1.18e-38f)));
   const float2 r = mul2(v, y);
   const float2 left = fma2(mul2(r, both(-1.f)), r, v);
-  return fma2(left, mul2(y, both(0.5f)), r);
+  const float2 root = fma2(left, mul2(y, both(0.5f)), r), below = mul2(v, both(0x1p-70f));
+  return make_float2(fmaxf(root.x, below.x), fmaxf(root.y, below.y));
 }
 // 1 / x to the nearest, by one Newton step.
 __device__ __forceinline__ float reciprocal(float x) {
@@ -283,6 +287,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         }
     }
     if constexpr (E8) {
+      if (left < 8) {  // 0 times an infinite scale is not 0
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j >= left) m[j] = r[j] = 0.f;
+      }
       float mt = 0.f, ml = fabsf(m[0]), rl = r[0];
       uint32_t rt = 0;
 #pragma unroll

@@ -110,3 +110,23 @@ def test_adamw_bf16_parameters_keep_a_nan(L, bits, gt):
         g[300] = bad
         L.AdamW(p, *L.AdamW.new_states(p, bits)).step([g], lr=1e-3)
         assert p[0][300].isnan() and int(p[0].isfinite().sum()) == 999
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("pt", [F32, BF])
+@pytest.mark.parametrize("at", [300, 900])
+def test_adamw_takes_no_step_where_the_second_moment_overflows(L, bits, pt, at):
+    """g = 1e21: v = 0.001 g^2 is infinite in fp32, sqrt(v) too, and m / sqrt(v) is 0."""
+    p = [rand(1, 1000, dtype=pt)]
+    start = p[0].clone()
+    g = rand(2, 1000, scale=1e-3)
+    g[at] = 1e21
+    opt = L.AdamW(p, *L.AdamW.new_states(p, bits), weight_decay=0.0)
+    for _ in range(3):
+        opt.step([g], lr=1e-3)
+        assert p[0].isfinite().all() and p[0][at] == start[at]
+    if bits == 32:
+        assert float(opt.v[0][at]) == float("inf") and opt.m[0].isfinite().all()
+    else:
+        assert opt.m_scale[0].isfinite().all() and opt.v_scale[0].isfinite().sum() == 3
+        assert bool((opt.v[0].view(torch.uint8)[at // 256 * 256:][:256] == 126).all())
