@@ -95,7 +95,8 @@ struct Step {
 };
 
 // sqrt(v) to the nearest: an approximate reciprocal root y, r = v y, and one step of the coupled
-// Newton iteration (Markstein), r + (v - r^2) y / 2.  v below 2^-126 counts as 0.  Of an infinite v that
+// Newton iteration (Markstein), r + (v - r^2) y / 2.  A subnormal v's root comes out too small, by up to
+// 2^-63: update() uses it only beside an e that hides that.  Of an infinite v the sum
 // is NaN (inf 0); v 2^-70, which is below the root of every finite v, is infinite there, and a maximum
 // takes the other operand of a NaN.  (A NaN v makes both NaN.)
 __device__ __forceinline__ float2 sqrt2(float2 v) {
@@ -114,14 +115,19 @@ __device__ __forceinline__ float reciprocal(float x) {
 }
 
 // Two elements: the new moments, sqrt(v), and the new parameters (whose fast reciprocal is good
-// to about 2^-22 of the step).
+// to about 2^-22 of the step).  EXACT: for an e below 2^-38; from there on an error of r of 2^-63 is within
+// the rounding of r + e.
+template <bool EXACT>
 __device__ __forceinline__ float2 update(const Step& h, float2 p, float2 g, float2& m, float2& v, float2& r) {
   g = mul2(g, both(h.scale));
   // x 1 + y: a packed addition of two packed products would be contracted to a fused operation
   // (which skips a rounding), a fused one is left alone
   m = fma2(mul2(m, both(h.beta1)), both(h.one), mul2(g, both(h.c1)));
   v = fma2(mul2(v, both(h.beta2)), both(h.one), mul2(mul2(g, both(h.c2)), g));
-  r = sqrt2(v);
+  if constexpr (EXACT)
+    r = make_float2(sqrtf(v.x), sqrtf(v.y));
+  else
+    r = sqrt2(v);
   const float2 den = add2(r, both(h.e));
   const float2 d = mul2(m, make_float2(rcp_approx(den.x), rcp_approx(den.y)));
   return fma2(both(-h.lr), fma2(d, both(h.a), mul2(p, both(h.decay))), p);
@@ -251,16 +257,23 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         m[j] = m2.x, m[j + 1] = m2.y, v[j] = v2.x, v[j + 1] = v2.y;
       }
     }
+    auto update8 = [&](auto exact) {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      float2 m2 = make_float2(m[j], m[j + 1]), v2 = make_float2(v[j], v[j + 1]), r2;
-      const float2 p2 =
-          update(h, make_float2(p[j], p[j + 1]), make_float2(g[j], g[j + 1]), m2, v2, r2);
-      p[j] = p2.x, p[j + 1] = p2.y;
-      m[j] = m2.x, m[j + 1] = m2.y;
-      v[j] = v2.x, v[j + 1] = v2.y;
-      r[j] = r2.x, r[j + 1] = r2.y;
-    }
+      for (int j = 0; j < 8; j += 2) {
+        float2 m2 = make_float2(m[j], m[j + 1]), v2 = make_float2(v[j], v[j + 1]), r2;
+        const float2 p2 =
+            update<decltype(exact)::value>(h, make_float2(p[j], p[j + 1]), make_float2(g[j], g[j + 1]), m2, v2, r2);
+        p[j] = p2.x, p[j + 1] = p2.y;
+        m[j] = m2.x, m[j + 1] = m2.y;
+        v[j] = v2.x, v[j + 1] = v2.y;
+        r[j] = r2.x, r[j + 1] = r2.y;
+      }
+    };
+    // (one branch for the eight, the same for the whole grid: one for every pair takes 4 % more of the kernel's time)
+    if (h.e >= 0x1p-38f)
+      update8(std::false_type{});
+    else
+      update8(std::true_type{});
     uint32_t rnd[8];
     if constexpr (E8 || sizeof(PT) == 2) {
       const uint32_t key = hash32(seed + 0x9E3779B9u * (sc.first + static_cast<uint32_t>(kt)));

@@ -4,7 +4,7 @@ Tolerances as in ``test_layers_gpu``."""
 import pytest
 
 torch = pytest.importorskip("torch")
-from test_layers_gpu import BF, E4, F32, L, rand  # noqa: F401,E402
+from test_layers_gpu import BF, E4, F32, F64, U32, L, check, f32, rand  # noqa: F401,E402
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +130,21 @@ def test_adamw_takes_no_step_where_the_second_moment_overflows(L, bits, pt, at):
     else:
         assert opt.m_scale[0].isfinite().all() and opt.v_scale[0].isfinite().sum() == 3
         assert bool((opt.v[0].view(torch.uint8)[at // 256 * 256:][:256] == 126).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [0.0, 1e-12])
+def test_adamw_divides_by_the_root_of_a_subnormal_second_moment(L, bits, eps):
+    """g = 3e-19: v = 9e-41 is a multiple of 2^-149.  The first step is lr m / (|g| + eps), m = g."""
+    p, g = [torch.zeros(1000, device="cuda")], torch.full((1000,), 3e-19, device="cuda")
+    g[::2] *= -1
+    opt = L.AdamW(p, *L.AdamW.new_states(p, bits), eps=eps, weight_decay=0.0)
+    opt.step([g], lr=1e-2)
+    v = 0.001 * float(g[1]) ** 2
+    want = -f32(1e-2) * g.to(F64) / (g.to(F64).abs() + f32(eps))
+    # the root halves v's relative error: three roundings of at most 2^-150 each
+    check("p", p[0], want, want.abs() * (1.5 * 2.0 ** -149 / v + 40 * U32))
+    r = opt.v[0].to(F64) * (opt.v_scale[0].to(F64).repeat_interleave(256)[:1000] if bits == 8 else 1)
+    want = v ** (0.5 if bits == 8 else 1)
+    if eps == 0:
+        check("v", r, torch.full_like(r, want), want * (3 * 2.0 ** -150 / v + 16 * U32))
