@@ -179,8 +179,10 @@ struct Raw8<uint8_t> {  // e4m3 codes
   __device__ __forceinline__ void get(float (&v)[8]) const { from_e4m3(q.x, v), from_e4m3(q.y, v + 4); }
 };
 
-// CAP: entries of the table; a small one keeps the argument block of a short list small.
-template <typename PT, typename GT, bool E8, int CAP>
+// CAP: entries of the table; a small one keeps the argument block of a short list small.  EXACT: a
+// kernel of its own, as a branch on it (the same for the whole grid) kept the loads' unpacking and
+// the update apart, 4 % of the time.
+template <typename PT, typename GT, bool E8, int CAP, bool EXACT>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> tab, const AdamScalars sc) {
   griddep_enter();
   const int lane = threadIdx.x & 31;
@@ -257,23 +259,16 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         m[j] = m2.x, m[j + 1] = m2.y, v[j] = v2.x, v[j + 1] = v2.y;
       }
     }
-    auto update8 = [&](auto exact) {
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        float2 m2 = make_float2(m[j], m[j + 1]), v2 = make_float2(v[j], v[j + 1]), r2;
-        const float2 p2 =
-            update<decltype(exact)::value>(h, make_float2(p[j], p[j + 1]), make_float2(g[j], g[j + 1]), m2, v2, r2);
-        p[j] = p2.x, p[j + 1] = p2.y;
-        m[j] = m2.x, m[j + 1] = m2.y;
-        v[j] = v2.x, v[j + 1] = v2.y;
-        r[j] = r2.x, r[j + 1] = r2.y;
-      }
-    };
-    // (one branch for the eight, the same for the whole grid: one for every pair takes 4 % more of the kernel's time)
-    if (h.e >= 0x1p-38f)
-      update8(std::false_type{});
-    else
-      update8(std::true_type{});
+    for (int j = 0; j < 8; j += 2) {
+      float2 m2 = make_float2(m[j], m[j + 1]), v2 = make_float2(v[j], v[j + 1]), r2;
+      const float2 p2 =
+          update<EXACT>(h, make_float2(p[j], p[j + 1]), make_float2(g[j], g[j + 1]), m2, v2, r2);
+      p[j] = p2.x, p[j + 1] = p2.y;
+      m[j] = m2.x, m[j + 1] = m2.y;
+      v[j] = v2.x, v[j + 1] = v2.y;
+      r[j] = r2.x, r[j + 1] = r2.y;
+    }
     uint32_t rnd[8];
     if constexpr (E8 || sizeof(PT) == 2) {
       const uint32_t key = hash32(seed + 0x9E3779B9u * (sc.first + static_cast<uint32_t>(kt)));
@@ -381,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   }
 }
 
-template <typename PT, typename GT, bool E8, int CAP>
+template <typename PT, typename GT, bool E8, int CAP, bool EXACT>
 cudaError_t launch(const AdamTensor* t, const AdamScalars& sc, cudaStream_t stream) {
   Table<CAP> tab;
   tab.first_block[0] = 0;
@@ -397,12 +392,14 @@ cudaError_t launch(const AdamTensor* t, const AdamScalars& sc, cudaStream_t stre
   const int64_t blocks = (tab.first_block[sc.n] + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks == 0) return cudaSuccess;
   const int64_t most = static_cast<int64_t>(current_sm_count()) * 8;
-  return launch_pdl(adamw_kernel<PT, GT, E8, CAP>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+  return launch_pdl(adamw_kernel<PT, GT, E8, CAP, EXACT>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
                     dim3(kThreads), 0, stream, 1, tab, sc);
 }
 template <typename PT, typename GT, bool E8>
 cudaError_t launch_cap(const AdamTensor* t, const AdamScalars& sc, cudaStream_t stream) {
-  return sc.n <= 32 ? launch<PT, GT, E8, 32>(t, sc, stream) : launch<PT, GT, E8, kAdamTensors>(t, sc, stream);
+  // eps sqrt(1 - beta2^t), at its least at the first step
+  if (sc.eps * sqrtf(sc.c2) < 0x1p-38f) return launch<PT, GT, E8, kAdamTensors, true>(t, sc, stream);
+  return sc.n <= 32 ? launch<PT, GT, E8, 32, false>(t, sc, stream) : launch<PT, GT, E8, kAdamTensors, false>(t, sc, stream);
 }
 template <typename PT, typename GT>
 cudaError_t launch_state(const AdamTensor* t, const AdamScalars& sc, int state_type, cudaStream_t stream) {
