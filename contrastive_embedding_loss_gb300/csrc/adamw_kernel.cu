@@ -24,6 +24,7 @@ namespace adam {
 
 constexpr int kThreads = 256;
 constexpr float kMinNormal = 0.015625f;  // 2^-6: e4m3's smallest normal number
+constexpr float kMinTop = 0x1p-116f;     // the least block maximum with codes: 448 / it is finite
 
 __device__ __forceinline__ uint32_t hash32(uint32_t x) {
   x ^= x >> 16;
@@ -311,6 +312,9 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       }
       mt = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(mt)));
       const float vt = __uint_as_float(__reduce_max_sync(~0u, rt));
+      // Momentum that is not fed halves every 7 steps (beta1 = 0.9) and gets here in some 750.  (A nonzero sqrt(v)
+      // is above 2^-75.)
+      if (mt < kMinTop) mt = 0.f;
       if (isnan(vt)) mt = vt;  // a NaN gradient makes both scales NaN
       const float mi = mt > 0.f ? reciprocal(mt) * 448.f : 0.f, vi = vt > 0.f ? reciprocal(vt) * 448.f : 0.f;
       if (lane == 0) {

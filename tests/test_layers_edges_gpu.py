@@ -4,7 +4,7 @@ Tolerances as in ``test_layers_gpu``."""
 import pytest
 
 torch = pytest.importorskip("torch")
-from test_layers_gpu import BF, E4, F32, F64, U32, L, check, f32, rand  # noqa: F401,E402
+from test_layers_gpu import BF, E4, F32, F64, U32, L, check, f32, rand, unpack  # noqa: F401,E402
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +148,22 @@ def test_adamw_divides_by_the_root_of_a_subnormal_second_moment(L, bits, eps):
     want = v ** (0.5 if bits == 8 else 1)
     if eps == 0:
         check("v", r, torch.full_like(r, want), want * (3 * 2.0 ** -150 / v + 16 * U32))
+
+
+def test_adamw_8bit_momentum_dies_out(L):
+    """Without gradients the momentum halves at every step (beta1 = 0.5).  A block whose largest is
+    below 2^-116 counts as 0."""
+    p, g = [rand(1, 512)], rand(2, 512, scale=1e-3)
+    g[256:] = 0
+    g[:256:3] = 0
+    opt = L.AdamW(p, *L.AdamW.new_states(p, 8), betas=(0.5, 0.999))
+    opt.step([g], lr=1e-3)
+    zero = torch.zeros_like(g)
+    for _ in range(140):
+        before = unpack(opt.m[0], opt.m_scale[0])
+        opt.step([zero], lr=1e-3)
+        m, unit = unpack(opt.m[0], opt.m_scale[0]), opt.m_scale[0].to(F64).repeat_interleave(256)
+        # less than one code away, or 0
+        check("m", m, before / 2, torch.maximum((before / 2).abs() * 2.0 ** -3, unit * 2.0 ** -9) * 1.0001 + 2.0 ** -116)
+        assert not m[before == 0].any()
+    assert not opt.m[0].to(F32).any() and not opt.m_scale[0].any()
