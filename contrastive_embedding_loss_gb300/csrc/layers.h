@@ -26,6 +26,7 @@ struct NormFwdParams {
   int width, x_type, stream_type, weight_type, y_type;
   float eps;
 };
+cudaError_t norm_kernels_setup();
 cudaError_t launch_norm_fwd(const NormFwdParams& p, cudaStream_t stream);
 
 struct NormRowsBwdParams {

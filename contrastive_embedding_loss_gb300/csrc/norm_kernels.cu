@@ -554,43 +554,62 @@ int64_t bwd_blocks(int64_t rows, int rows_per_block, int per_sm) {
   const int64_t n = turns <= some ? turns : turns / 4 < some ? some : turns / 4 / 8 * 8;
   return n < 1 ? 1 : n < most ? n : most;
 }
+constexpr int kMostRing = 220 * 1024;  // bytes, beside the static arrays
 template <typename GT, typename ST, int TPR, int N>
 cudaError_t bwd_async(const NormRowsBwdParams& p, int64_t* blocks, cudaStream_t stream) {
   constexpr int kBlock = bwd_block<TPR>();
   const int chunks = (p.width / 8 + TPR - 1) / TPR;
   const int stage = chunks * static_cast<int>(8 * (sizeof(GT) + sizeof(ST) * (p.ds ? 2 : 1))) * kBlock;
-  const int stages = 2 * stage <= 220 * 1024 ? 2 : 1;  // (one: rows of more than 8192 fp32 values)
+  const int stages = 2 * stage <= kMostRing ? 2 : 1;  // (one: the longest rows with fp32 dy or stream)
   const int smem = stages * stage;
   // fp32 arrays need room in L1 for the other half of their sectors
   int per_sm = (sizeof(GT) + sizeof(ST) > 4 ? 168 : 220) * 1024 / (smem + 2 * 1024);
   per_sm = per_sm < bwd_per_sm<TPR, N>() ? per_sm : bwd_per_sm<TPR, N>();
   per_sm = per_sm < 1 ? 1 : per_sm > kMostBlocksPerSm ? kMostBlocksPerSm : per_sm;
   *blocks = bwd_blocks(p.rows, kBlock / TPR, per_sm);
-  if (smem > 40 * 1024) {  // past 48 KB together with the static arrays
-    const cudaError_t e =
-        cudaFuncSetAttribute(bwd_kernel<GT, ST, TPR, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
   return launch_pdl(bwd_kernel<GT, ST, TPR, N>, dim3(static_cast<unsigned>(*blocks)), dim3(kBlock), smem, stream, 1, p, chunks,
                     stages);
 }
+// Calls f with the variant for a width.
+template <int TPR, int N>
+struct Variant {
+  static constexpr int kTpr = TPR, kValues = N;
+};
+template <typename ST, typename F>
+cudaError_t for_width(int width, F&& f) {
+  if constexpr (sizeof(ST) == 2) {
+    if (width <= 1024) return f(Variant<32, 32>{});
+    if (width <= 4096) return f(Variant<128, 32>{});
+    if (width <= 8192) return f(Variant<256, 32>{});
+    return f(Variant<512, 32>{});
+  } else {
+    if (width <= 512) return f(Variant<32, 16>{});
+    if (width <= 1024) return f(Variant<64, 16>{});
+    if (width <= 2048) return f(Variant<128, 16>{});
+    if (width <= 4096) return f(Variant<256, 16>{});
+    if (width <= 8192) return f(Variant<512, 16>{});
+    return f(Variant<1024, 16>{});
+  }
+}
+// Every variant may take the largest ring: the limit is the function's, not a call's, so a call that
+// set its own would race with other threads'.
+template <typename GT, typename ST>
+cudaError_t bwd_setup() {
+  for (int width = 512; width <= kNormMaxWidth; width *= 2) {
+    const cudaError_t e = for_width<ST>(width, [](auto v) {
+      return cudaFuncSetAttribute(bwd_kernel<GT, ST, decltype(v)::kTpr, decltype(v)::kValues>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kMostRing);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 template <typename GT, typename ST>
 cudaError_t bwd(const NormRowsBwdParams& p, bool vec, int64_t* blocks, cudaStream_t stream) {
-  if (vec) {
-    if constexpr (sizeof(ST) == 2) {
-      if (p.width <= 1024) return bwd_async<GT, ST, 32, 32>(p, blocks, stream);
-      if (p.width <= 4096) return bwd_async<GT, ST, 128, 32>(p, blocks, stream);
-      if (p.width <= 8192) return bwd_async<GT, ST, 256, 32>(p, blocks, stream);
-      return bwd_async<GT, ST, 512, 32>(p, blocks, stream);
-    } else {
-      if (p.width <= 512) return bwd_async<GT, ST, 32, 16>(p, blocks, stream);
-      if (p.width <= 1024) return bwd_async<GT, ST, 64, 16>(p, blocks, stream);
-      if (p.width <= 2048) return bwd_async<GT, ST, 128, 16>(p, blocks, stream);
-      if (p.width <= 4096) return bwd_async<GT, ST, 256, 16>(p, blocks, stream);
-      if (p.width <= 8192) return bwd_async<GT, ST, 512, 16>(p, blocks, stream);
-      return bwd_async<GT, ST, 1024, 16>(p, blocks, stream);
-    }
-  }
+  if (vec)
+    return for_width<ST>(p.width, [&](auto v) {
+      return bwd_async<GT, ST, decltype(v)::kTpr, decltype(v)::kValues>(p, blocks, stream);
+    });
   const int tpr = threads_per_row(p.width);
   *blocks = bwd_blocks(p.rows, tpr == 32 ? 4 : 1, tpr == 512 ? 1 : tpr == 256 ? 2 : 4);
   const dim3 grid(static_cast<unsigned>(*blocks));
@@ -608,6 +627,13 @@ cudaError_t launch_norm_fwd(const NormFwdParams& p, cudaStream_t stream) {
   const bool w = aligned16(p.weight) && in_step(p.y, p.ldy, elem_of(p.y_type), p.x, p.ldx, xe) &&
                  (!p.res || (in_step(p.res, p.ldr, se, p.x, p.ldx, xe) && in_step(p.s, p.lds, se, p.x, p.ldx, xe)));
   return w ? fwd_types<8>(p, stream) : fwd_types<1>(p, stream);
+}
+
+cudaError_t norm_kernels_setup() {
+  cudaError_t e = norm::bwd_setup<float, float>();
+  if (e == cudaSuccess) e = norm::bwd_setup<float, uint16_t>();
+  if (e == cudaSuccess) e = norm::bwd_setup<uint16_t, float>();
+  return e == cudaSuccess ? norm::bwd_setup<uint16_t, uint16_t>() : e;
 }
 
 int64_t norm_bwd_blocks(int64_t rows, int width) {

@@ -340,7 +340,8 @@ uf_status_t uf_contrastive_init(int device) {
     st = UF_CUDA_ERROR;
   } else if (wgt_kernel_setup() != cudaSuccess || gemm_kernel_setup() != cudaSuccess ||
              fwd_kernel_setup() != cudaSuccess ||
-             aux_kernels_setup() != cudaSuccess || dense_kernel_setup() != cudaSuccess || !get_encode()) {
+             aux_kernels_setup() != cudaSuccess || dense_kernel_setup() != cudaSuccess ||
+             norm_kernels_setup() != cudaSuccess || !get_encode()) {
     st = UF_CUDA_ERROR;
   }
   if (st == UF_OK && cudaDeviceGetAttribute(&g_sm_count[device], cudaDevAttrMultiProcessorCount, device) != cudaSuccess)

@@ -1,6 +1,8 @@
 """The head's operators and the optimizer where they can go wrong beside the ordinary sizes: replaced
 storage, the ends of the formats' ranges, sides of a limit, calls from threads and other streams.
 Tolerances as in ``test_layers_gpu``."""
+import threading
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -167,3 +169,32 @@ def test_adamw_8bit_momentum_dies_out(L):
         check("m", m, before / 2, torch.maximum((before / 2).abs() * 2.0 ** -3, unit * 2.0 ** -9) * 1.0001 + 2.0 ** -116)
         assert not m[before == 0].any()
     assert not opt.m[0].to(F32).any() and not opt.m_scale[0].any()
+
+
+# ------------------------------------------------------------------------------- RMS norm
+
+def test_rmsnorm_backward_from_two_threads(L):
+    """Calls with and without d_stream need rings of different sizes of one kernel; calls from two
+    threads may interleave at any point.  (ctypes lets go of the interpreter's lock.)"""
+    rows, width, lib = 4, 8192, L._load()
+    refused = []
+
+    def calls(carry, seed):
+        s, dy, w = rand(seed, rows, width), rand(seed + 1, rows, width), rand(seed + 2, width)
+        rstd, dx = torch.ones(rows, device="cuda"), torch.empty(rows, width, device="cuda")
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        bad = 0
+        for _ in range(3000):
+            bad += 0 != lib.uf_rmsnorm_bwd(dy.data_ptr(), width, 1, s.data_ptr(), width, 1, w.data_ptr(), 1, rstd.data_ptr(),
+                                           s.data_ptr() if carry else None, width, rows, width, dx.data_ptr(), width, None,
+                                           None, 0, stream.cuda_stream)
+        stream.synchronize()
+        refused.append(bad)
+
+    threads = [threading.Thread(target=calls, args=(carry, 10 * carry)) for carry in (False, True)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert refused == [0, 0]
