@@ -174,10 +174,12 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) fwd_kernel(const NormFw
   q = row_sum<TPR>(q, red);
   const float rho = rsqrtf(q / static_cast<float>(p.width) + p.eps);
   if (p.rstd && lane == 0) p.rstd[row] = rho;
-  // bf16: y = s (rho w).  e4m3: the codes 448 y / max |y| do not depend on rho, which is left to the
-  // row's scale: one rounding less before the code is chosen.
+  // bf16: y = s (rho w).  e4m3: the codes 448 y / max |y| do not depend on rho, of which only the power
+  // of two goes into y, the rest into the row's scale: one rounding less before the code is chosen, at
+  // y's own size.  (A rho of 0, infinity or NaN goes to the scale.)
   const bool e4m3 = p.y_type == kE4m3;
-  const float by = e4m3 ? 1.f : rho;
+  const float two = rho > 0.f && rho < __int_as_float(0x7F800000) ? __uint_as_float(__float_as_uint(rho) & 0x7F800000u) : 1.f;
+  const float by = e4m3 ? two : rho;
   if (cut.extra >= 0) e *= by * weight1(p.weight, p.weight_type, cut.extra);
   float top = fabsf(e);
 #pragma unroll
@@ -204,8 +206,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) fwd_kernel(const NormFw
     return;
   }
   top = row_max<TPR>(top, red);
-  const float inv = top > 0.f ? 448.f / top : 1.f;
-  if (lane == 0) p.y_scale[row] = rho * top / 448.f;
+  // (of a row whose y are all below 2^-116 the quotient is infinite: they count as zeros)
+  if (top < 0x1p-116f) top = 0.f;
+  const float inv = top > 0.f ? 448.f / top : 0.f;
+  if (lane == 0) p.y_scale[row] = rho / two * top / 448.f;
   uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.ldy;
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {

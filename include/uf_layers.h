@@ -42,7 +42,8 @@ typedef enum uf_activation {
  *   residual     [rows][width] of stream_type (UF_BF16 or UF_F32), or NULL.
  *   weight       [width], weight_type UF_BF16 or UF_F32.
  *   y            [rows][width], y_type UF_BF16, or UF_E4M3: then y = e4m3(448 y / a) with
- *                a = max |y| over the row, and y_scale[row] = a / 448 (a row of zeros: 0, codes 0).
+ *                a = max |y| over the row, and y_scale[row] = a / 448 (a row of zeros, or with
+ *                a < 2^-116: 0, codes 0).
  *   stream_out   [rows][width] of stream_type: s (needed with a residual, NULL without).
  *   rstd         [rows] or NULL: rho, for the backward.
  * 1 <= width <= 16384, any width and alignment of the elements' own size; rows of 16 bytes'

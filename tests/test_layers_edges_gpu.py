@@ -198,3 +198,41 @@ def test_rmsnorm_backward_from_two_threads(L):
     for t in threads:
         t.join()
     assert refused == [0, 0]
+
+
+@pytest.mark.parametrize("width", [77, 520, 5000])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_rmsnorm_e4m3_rows_of_tiny_values(L, width, dtype):
+    """y is up to 1000 times s (rho = eps^-1/2): rows whose s are below 448 / 2^128 have a larger y."""
+    x = rand(1, 6, width) * torch.tensor([1e-36, 1e-37, 2e-38, 1.0, 1e-30, 0.0], device="cuda")[:, None]
+    x = x.to(dtype)
+    x[:, 1::3] = 0
+    w = 1 + rand(2, width, scale=0.1)
+    got = L.rmsnorm_fwd(x, w, eps=1e-6, out="e4m3")
+    y = x.to(F64) * (x.to(F64).square().mean(1, keepdim=True) + 1e-6).rsqrt() * w.to(F64)
+    top, rel = y.abs().amax(1), (width / 2 + 24) * U32
+    check("scale", got["scale"], top / 448, top / 448 * (rel + 4 * U32))
+    scale = got["scale"].to(F64)[:, None]
+    check("y", got["y"].to(F64) * scale, y, torch.maximum(y.abs() * 2.0 ** -4, scale * 2.0 ** -10) * 1.001 + y.abs() * rel)
+
+
+def test_rmsnorm_e4m3_rows_below_the_range_count_as_zeros(L):
+    x = rand(1, 3, 200)
+    x[1] *= 1e-41
+    x[1, ::2] = 0
+    got = L.rmsnorm_fwd(x, torch.ones(200, device="cuda"), eps=1e-6, out="e4m3")
+    assert float(got["scale"][1]) == 0 and not got["y"][1].to(F32).any()
+    assert bool((got["scale"][::2] > 0).all())
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan"), 1e30])
+def test_rmsnorm_e4m3_marks_a_non_finite_row(L, bad):
+    """An infinity or a NaN makes its row's products NaN, as the formula does; where only the mean of
+    squares overflows, rho is 0 and so is the row."""
+    x = rand(1, 3, 520)
+    clean = L.rmsnorm_fwd(x, torch.ones(520, device="cuda"), out="e4m3")
+    x[1, 100] = bad
+    got = L.rmsnorm_fwd(x, torch.ones(520, device="cuda"), out="e4m3")
+    y = got["y"].to(F32) * got["scale"][:, None]
+    assert torch.equal(got["y"].view(torch.uint8)[::2], clean["y"].view(torch.uint8)[::2])
+    assert y[1].isnan().all() if bad != 1e30 else not y[1].any()
