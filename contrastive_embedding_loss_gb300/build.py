@@ -2,8 +2,9 @@
 
 nvcc compiles each translation unit for sm_103a only (in parallel), then links one
 shared object with the CUDA runtime linked statically, so loading the library needs no
-GPU and no libcuda (the driver entry point is resolved at the first call).  Beside it, g++
-builds ``_layers_native.so``, the Python module that calls the library with torch tensors.
+GPU and no libcuda (the driver entry point is resolved at the first call).  The library needs
+nvcc alone.  Where torch is installed, g++ builds ``_layers_native.so`` beside it, the Python
+module that calls the library with torch tensors.
 """
 from __future__ import annotations
 
@@ -37,7 +38,7 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _digest() -> str:
+def _digest(*more: str) -> str:
     h = hashlib.sha1()
     for d in (CSRC, INCLUDE):
         for f in sorted(os.listdir(d)):
@@ -45,8 +46,19 @@ def _digest() -> str:
                 h.update(f.encode() + fh.read())
     h.update(" ".join(ARCH + FLAGS).encode())
     h.update(os.uname().machine.encode())
-    h.update(importlib.metadata.version("torch").encode())
+    h.update(" ".join(more).encode())
     return h.hexdigest()[:16]
+
+
+def _fresh(out: str, digest: str) -> bool:
+    """Whether ``out`` was built from what ``digest`` stands for."""
+    stamp = out + ".stamp"
+    return os.path.exists(out) and os.path.exists(stamp) and open(stamp).read() == digest
+
+
+def _stamp(out: str, digest: str) -> None:
+    with open(out + ".stamp", "w") as f:
+        f.write(digest)
 
 
 def lib_path() -> str:
@@ -57,10 +69,16 @@ def native_path() -> str:
     return os.path.join(BUILD, NATIVE_NAME)
 
 
-def _build_native() -> None:
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
-    cuda = os.path.dirname(os.path.dirname(nvcc()))
+def _build_native(force: bool) -> None:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return
     out = native_path()
+    digest = _digest(importlib.metadata.version("torch"))
+    if not force and _fresh(out, digest):
+        return
+    torch_dir = os.path.dirname(spec.origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = out + f".tmp{os.getpid()}"
     include = [f"{torch_dir}/include", f"{torch_dir}/include/torch/csrc/api/include", f"{cuda}/include",
                sysconfig.get_paths()["include"]]
@@ -71,17 +89,13 @@ def _build_native() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {NATIVE_SOURCE}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, out)
+    _stamp(out, digest)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (when sources changed) and return the path of the shared library."""
-    os.makedirs(BUILD, exist_ok=True)
-    stamp = os.path.join(BUILD, "stamp.txt")
-    digest = _digest()
-    out = lib_path()
-    if (not force and os.path.exists(out) and os.path.exists(native_path()) and os.path.exists(stamp)
-            and open(stamp).read() == digest):
-        return out
+def _build_library(force: bool, verbose: bool) -> None:
+    out, digest = lib_path(), _digest()
+    if not force and _fresh(out, digest):
+        return
     exe = nvcc()
 
     def compile_one(src):
@@ -94,19 +108,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        native = ex.submit(_build_native)
+    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        native.result()
     tmp = out + f".tmp{os.getpid()}"
     cmd = [exe, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, out)
-    with open(stamp, "w") as f:
-        f.write(digest)
-    return out
+    _stamp(out, digest)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile what is not up to date and return the path of the shared library."""
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(1) as ex:
+        native = ex.submit(_build_native, force)
+        _build_library(force, verbose)
+        native.result()
+    return lib_path()
 
 
 if __name__ == "__main__":

@@ -1,6 +1,9 @@
 """Host-side edges of the head's operators (no GPU needed)."""
 import ctypes
+import importlib.metadata
+import os
 import random
+import subprocess
 
 import pytest
 
@@ -52,3 +55,47 @@ def test_adamw_refuses_overlaps_across_tensors(lib):
                 continue
             args = [moved[k] for k in (p, g, m, v)]
             assert _adamw(lib, *args, sizes, moved[ms], moved[vs], moved[c]) == INV, (order, a, i, b, j)
+
+
+@pytest.fixture
+def compilers(tmp_path, monkeypatch):
+    """build.py on an empty folder, with compilers that only write their output file; the list of their calls."""
+    from contrastive_embedding_loss_gb300 import build
+
+    calls = []
+
+    def run(cmd, **kw):
+        calls.append(os.path.basename(cmd[0]))
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            pass
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "nvcc", lambda: "nvcc")
+    monkeypatch.setattr(build.subprocess, "run", run)
+    return build, calls, monkeypatch
+
+
+def test_the_library_builds_without_torch(compilers):
+    build, calls, monkeypatch = compilers
+
+    def missing(name):
+        raise importlib.metadata.PackageNotFoundError(name)
+
+    monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: None)
+    monkeypatch.setattr(build.importlib.metadata, "version", missing)
+    out = build.build()
+    assert os.path.exists(out) and not os.path.exists(build.native_path())
+    assert calls == ["nvcc"] * (len(build.SOURCES) + 1)
+
+
+def test_another_torch_rebuilds_the_binding_alone(compilers):
+    build, calls, monkeypatch = compilers
+    build.build()
+    assert sorted(calls) == ["g++"] + ["nvcc"] * (len(build.SOURCES) + 1) and os.path.exists(build.native_path())
+    calls.clear()
+    build.build()
+    assert calls == []
+    monkeypatch.setattr(build.importlib.metadata, "version", lambda name: "0.0.1")
+    build.build()
+    assert calls == ["g++"]
