@@ -3,8 +3,9 @@
 nvcc compiles each translation unit for sm_103a only (in parallel), then links one
 shared object with the CUDA runtime linked statically, so loading the library needs no
 GPU and no libcuda (the driver entry point is resolved at the first call).  The library needs
-nvcc alone.  Where torch is installed, g++ builds ``_layers_native.so`` beside it, the Python
-module that calls the library with torch tensors.
+nvcc alone.  Where torch is installed, g++ builds ``_layers_native-<torch's version>.so`` beside
+it, the Python module that calls the library with torch tensors: one that was built against
+another torch is not found, rather than loaded.
 """
 from __future__ import annotations
 
@@ -24,7 +25,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB_NAME = "libuf_contrastive.so"
 SOURCES = ["wgt_kernel.cu", "gemm_kernel.cu", "fwd_kernel.cu", "aux_kernels.cu", "uf_contrastive.cu", "uf_static.cu",
            "dense_kernel.cu", "skinny_kernel.cu", "norm_kernels.cu", "act_kernels.cu", "adamw_kernel.cu", "uf_layers.cu"]
-NATIVE_NAME = "_layers_native.so"
+NATIVE_NAME = "_layers_native"
 NATIVE_SOURCE = "layers_binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -65,8 +66,15 @@ def lib_path() -> str:
     return os.path.join(BUILD, LIB_NAME)
 
 
+def torch_version() -> str:
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return "none"
+
+
 def native_path() -> str:
-    return os.path.join(BUILD, NATIVE_NAME)
+    return os.path.join(BUILD, f"{NATIVE_NAME}-{torch_version()}.so")
 
 
 def _build_native(force: bool) -> None:
@@ -74,7 +82,7 @@ def _build_native(force: bool) -> None:
     if spec is None:
         return
     out = native_path()
-    digest = _digest(importlib.metadata.version("torch"))
+    digest = _digest(torch_version())
     if not force and _fresh(out, digest):
         return
     torch_dir = os.path.dirname(spec.origin)

@@ -63,7 +63,7 @@ def _load() -> ctypes.CDLL:
 def _load_native():
     path = _build.native_path()
     if not os.path.exists(path):
-        raise ImportError(f"the native binding is not built ({path} is missing); "
+        raise ImportError(f"the native binding is not built for this torch ({path} is missing); "
                           "run `python -c 'import __graft_entry__ as g; g.build()'`")
     loader = importlib.machinery.ExtensionFileLoader("_layers_native", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_layers_native", loader))

@@ -99,3 +99,13 @@ def test_another_torch_rebuilds_the_binding_alone(compilers):
     monkeypatch.setattr(build.importlib.metadata, "version", lambda name: "0.0.1")
     build.build()
     assert calls == ["g++"]
+
+
+def test_a_binding_of_another_torch_is_not_loaded(lib, monkeypatch):
+    from contrastive_embedding_loss_gb300 import layers
+
+    assert layers._load_native() is not None
+    version = importlib.metadata.version
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.0.1" if name == "torch" else version(name))
+    with pytest.raises(ImportError, match="not built for this torch"):
+        layers._load_native()
