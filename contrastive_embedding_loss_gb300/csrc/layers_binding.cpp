@@ -9,12 +9,14 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
+#include <optional>
 #include <string>
 #include <type_traits>
 #include <vector>
@@ -151,11 +153,14 @@ struct Scratch {
 
 // The tensors' device made current for a call, and the stream to call on: the caller's (a
 // torch.cuda.Stream), made current too, so that outputs and scratch are allocated on the stream
-// that uses them and scratch that is freed on return goes back to it; or the current one.
+// that uses them and scratch that is freed on return goes back to it; or the current one.  What the
+// caller hands to a call on another stream than its own is marked as used there (uses), so that
+// memory that the caller frees after the call is not given away before the kernels have run.
 struct On {
   c10::cuda::OptionalCUDAStreamGuard stream_guard;
   c10::cuda::OptionalCUDAGuard guard;
   void* stream;
+  std::optional<c10::cuda::CUDAStream> other;  // the stream, if it is not the current one
   On(const c10::Device& dev, PyObject* s) {
     if (given(s)) {
       const auto part = [&](const char* name) {
@@ -169,12 +174,33 @@ struct On {
       const auto cs = c10::cuda::CUDAStream::unpack3(part("stream_id"), static_cast<c10::DeviceIndex>(part("device_index")),
                                                      static_cast<c10::DeviceType>(part("device_type")));
       if (cs.device() != dev) raise(PyExc_ValueError, "stream must be on %s, not %s", dev.str().c_str(), cs.device().str().c_str());
+      if (cs != c10::cuda::getCurrentCUDAStream(dev.index())) other = cs;
       stream_guard.reset_stream(cs);
       stream = cs.stream();
       return;
     }
     if (c10::cuda::current_device() != dev.index()) guard.set_device(dev);
     stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+  }
+  // The tensors among a call's arguments, and those of its lists.
+  void uses(PyObject* const* args, int n) const {
+    if (!other) return;
+    for (int i = 0; i < n; ++i) {
+      if (THPVariable_Check(args[i])) {
+        const Tensor& t = THPVariable_Unpack(args[i]);
+        if (t.is_cuda()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *other);
+      } else if (PyList_Check(args[i])) {
+        for (Py_ssize_t k = 0; k < PyList_GET_SIZE(args[i]); ++k) {
+          PyObject* item = PyList_GET_ITEM(args[i], k);
+          uses(&item, 1);
+        }
+      } else if (PyTuple_Check(args[i])) {
+        for (Py_ssize_t k = 0; k < PyTuple_GET_SIZE(args[i]); ++k) {
+          PyObject* item = PyTuple_GET_ITEM(args[i], k);
+          uses(&item, 1);
+        }
+      }
+    }
   }
 };
 
@@ -227,6 +253,7 @@ PyObject* rmsnorm_fwd(PyObject* const* a) {
                         e4m3 ? UF_E4M3 : UF_BF16, static_cast<float*>(opt(scale)), opt(s), width,
                         static_cast<float*>(rstd.data_ptr()), on.stream),
         "uf_rmsnorm_fwd");
+  on.uses(a, 6);
   Result out;
   out.put("y", y);
   out.put("rstd", rstd);
@@ -256,6 +283,7 @@ PyObject* rmsnorm_bwd(PyObject* const* a) {
                         carry ? ld(ds) : 0, rows, static_cast<int>(width), dx.data_ptr(), width, static_cast<float*>(opt(dw)),
                         ws.ptr, ws.bytes, on.stream),
         "uf_rmsnorm_bwd");
+  on.uses(a, 8);
   Result out;
   out.put("dx", dx);
   if (grad) out.put("dweight", dw);
@@ -298,6 +326,7 @@ PyObject* linear_fwd(PyObject* const* a) {
                        r.defined() ? ld(r) : 0, static_cast<int>(integer(a[3])), rows, static_cast<int>(inner),
                        static_cast<int>(outer), y.data_ptr(), outer, opt(pre), outer, ws.ptr, ws.bytes, ws.status, on.stream),
         "uf_linear_fwd");
+  on.uses(a, 11);
   Result out;
   out.put("y", y);
   if (pre.defined()) out.put("pre", pre);
@@ -326,6 +355,7 @@ PyObject* linear_bwd(PyObject* const* a) {
                        act ? ld(pre) : 0, act, rows, static_cast<int>(inner), static_cast<int>(outer), opt(dx), inner,
                        opt(dw), inner, static_cast<float*>(opt(db)), ws.ptr, ws.bytes, ws.status, on.stream),
         "uf_linear_bwd");
+  on.uses(a, 11);
   Result out;
   if (dx.defined()) out.put("dx", dx);
   if (dw.defined()) out.put("dW", dw);
@@ -358,6 +388,7 @@ PyObject* gated_fwd(PyObject* const* a) {
                       static_cast<int>(inner), static_cast<int>(outer), h.data_ptr(), outer, opt(pre), 2 * outer, ws.ptr,
                       ws.bytes, ws.status, on.stream),
         "uf_gated_fwd");
+  on.uses(a, 7);
   Result out;
   out.put("h", h);
   if (pre.defined()) out.put("pre", pre);
@@ -382,6 +413,7 @@ PyObject* gated_bwd(PyObject* const* a) {
                       static_cast<int>(integer(a[4])), rows, static_cast<int>(inner), static_cast<int>(outer), opt(dx),
                       inner, opt(dw), inner, ws.ptr, ws.bytes, ws.status, on.stream),
         "uf_gated_bwd");
+  on.uses(a, 10);
   Result out;
   if (dx.defined()) out.put("dx", dx);
   if (dw.defined()) out.put("dW", dw);
@@ -514,6 +546,7 @@ PyObject* adamw_step(PyObject* const* a) {
                        static_cast<float>(number(a[4])), static_cast<float>(number(a[5])), integer(a[6]), step_dev,
                        static_cast<uint32_t>(integer(a[8])), gs, on.stream),
         "uf_adamw_step");
+  on.uses(a - 6, 17);
   Py_RETURN_NONE;
 }
 

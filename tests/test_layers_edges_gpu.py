@@ -236,3 +236,46 @@ def test_rmsnorm_e4m3_marks_a_non_finite_row(L, bad):
     y = got["y"].to(F32) * got["scale"][:, None]
     assert torch.equal(got["y"].view(torch.uint8)[::2], clean["y"].view(torch.uint8)[::2])
     assert y[1].isnan().all() if bad != 1e30 else not y[1].any()
+
+
+# ---------------------------------------------------------------------------- other streams
+
+def test_inputs_of_a_call_on_another_stream_may_be_freed(L):
+    """Calls that wait behind a long kernel on their stream; their inputs are freed and as much memory
+    is allocated and overwritten on the current stream meanwhile."""
+    args = {"x": rand(1, 300, 512, dtype=BF), "w": rand(2, 256, 512, scale=0.05, dtype=BF), "n": rand(3, 512),
+            "r": rand(4, 300, 512), "dy": rand(5, 300, 256, dtype=BF), "pre": rand(6, 300, 256, dtype=BF),
+            "dh": rand(7, 300, 128, dtype=BF), "rstd": rand(8, 300).abs(), "p": rand(9, 1 << 16), "g": rand(10, 1 << 16),
+            "lr": torch.full((1,), 0.5, device="cuda")}
+    passes = {
+        "rmsnorm_fwd": (lambda a, s: L.rmsnorm_fwd(a["x"], a["n"], residual=a["r"], stream=s), "x n r"),
+        "rmsnorm_bwd": (lambda a, s: L.rmsnorm_bwd(a["x"], a["r"], a["n"], a["rstd"], d_stream=a["r"], stream=s), "x r n rstd"),
+        "linear_fwd": (lambda a, s: L.linear_fwd(a["x"], a["w"], bias=a["n"][:256], residual=a["dy"], stream=s), "x w n dy"),
+        "linear_bwd": (lambda a, s: L.linear_bwd(a["dy"], a["x"], a["w"], pre=a["pre"], act="gelu", stream=s), "dy x w pre"),
+        "gated_fwd": (lambda a, s: L.gated_fwd(a["x"], a["w"], stream=s), "x w"),
+        "gated_bwd": (lambda a, s: L.gated_bwd(a["dh"], a["x"], a["w"], a["pre"], stream=s), "dh x w pre"),
+    }
+
+    def adamw(a, s):
+        opt = L.AdamW([a["p"]], *L.AdamW.new_states([a["p"]]))
+        if s is not None:
+            s.wait_stream(torch.cuda.current_stream())  # (the states)
+        opt.step((a["g"],), lr=a["lr"], stream=s)
+        return {"p": a["p"]}
+
+    passes["adamw"] = (adamw, "g lr")
+    side = torch.cuda.Stream()
+    for name, (call, names) in passes.items():
+        want = call({k: t.clone() for k, t in args.items()}, None)
+        a = {k: t.clone() for k, t in args.items()}
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = call(a, side)
+        freed = [(a[k].shape, a[k].dtype) for k in names.split()]
+        for k in names.split():
+            del a[k]
+        junk = [torch.full(shape, float("nan"), dtype=dtype, device="cuda") for shape, dtype in freed]
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], want[k]) for k in want), name
+        del junk
