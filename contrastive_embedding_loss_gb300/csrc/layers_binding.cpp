@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
+#include <limits>
 #include <optional>
 #include <string>
 #include <type_traits>
@@ -95,6 +96,13 @@ const Tensor& vector(const char* name, PyObject* o, Types types, const c10::Devi
   if (t.device() != dev || t.dim() != 1 || t.size(0) != n || (n > 1 && t.stride(0) != 1))
     raise(PyExc_ValueError, "%s must be a contiguous vector of %lld on %s", name, static_cast<long long>(n), dev.str().c_str());
   return t;
+}
+
+// A matrix's width, an int in the C entry points.
+int width_of(const char* name, int64_t n) {
+  if (n > std::numeric_limits<int>::max())
+    raise(PyExc_ValueError, "%s may be at most %d, not %lld", name, std::numeric_limits<int>::max(), static_cast<long long>(n));
+  return static_cast<int>(n);
 }
 
 // Row stride in elements (a single row has none of its own).
@@ -236,7 +244,8 @@ void* opt(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 PyObject* rmsnorm_fwd(PyObject* const* a) {
   const bool res = given(a[2]), e4m3 = truth(a[4]);
   const Tensor& x = matrix("x", a[0], res ? kBf16 : kFloats);
-  const int64_t rows = x.size(0), width = x.size(1);
+  const int64_t rows = x.size(0);
+  const int width = width_of("x's width", x.size(1));
   const c10::Device dev = x.device();
   const Tensor& w = vector("weight", a[1], kFloats, dev, width);
   const Tensor none;
@@ -249,7 +258,7 @@ PyObject* rmsnorm_fwd(PyObject* const* a) {
   if (e4m3) scale = empty({rows}, at::kFloat, dev);
   check(api.rmsnorm_fwd(x.data_ptr(), ld(x), type_of(x.scalar_type()), opt(r), res ? ld(r) : 0,
                         res ? type_of(r.scalar_type()) : 0, w.data_ptr(), type_of(w.scalar_type()), rows,
-                        static_cast<int>(width), static_cast<float>(number(a[3])), y.data_ptr(), width,
+                        width, static_cast<float>(number(a[3])), y.data_ptr(), width,
                         e4m3 ? UF_E4M3 : UF_BF16, static_cast<float*>(opt(scale)), opt(s), width,
                         static_cast<float*>(rstd.data_ptr()), on.stream),
         "uf_rmsnorm_fwd");
@@ -265,7 +274,8 @@ PyObject* rmsnorm_fwd(PyObject* const* a) {
 // dy, s, weight, rstd, d_stream, weight_grad, workspace, stream
 PyObject* rmsnorm_bwd(PyObject* const* a) {
   const Tensor& s = matrix("s", a[1], kFloats);
-  const int64_t rows = s.size(0), width = s.size(1);
+  const int64_t rows = s.size(0);
+  const int width = width_of("s's width", s.size(1));
   const c10::Device dev = s.device();
   const Tensor& dy = matrix("dy", a[0], kFloats, &dev, rows, width);
   const Tensor& w = vector("weight", a[2], kFloats, dev, width);
@@ -277,10 +287,10 @@ PyObject* rmsnorm_bwd(PyObject* const* a) {
   const Tensor dx = empty({rows, width}, s.scalar_type(), dev);
   Tensor dw;
   if (grad) dw = empty({width}, at::kFloat, dev);
-  const Scratch ws(grad ? api.rmsnorm_bwd_workspace(rows, static_cast<int>(width)) : 0, dev, a[6], Py_None);
+  const Scratch ws(grad ? api.rmsnorm_bwd_workspace(rows, width) : 0, dev, a[6], Py_None);
   check(api.rmsnorm_bwd(dy.data_ptr(), ld(dy), type_of(dy.scalar_type()), s.data_ptr(), ld(s), type_of(s.scalar_type()),
                         w.data_ptr(), type_of(w.scalar_type()), static_cast<const float*>(rstd.data_ptr()), opt(ds),
-                        carry ? ld(ds) : 0, rows, static_cast<int>(width), dx.data_ptr(), width, static_cast<float*>(opt(dw)),
+                        carry ? ld(ds) : 0, rows, width, dx.data_ptr(), width, static_cast<float*>(opt(dw)),
                         ws.ptr, ws.bytes, on.stream),
         "uf_rmsnorm_bwd");
   on.uses(a, 8);
@@ -303,10 +313,11 @@ const Tensor& weight_of(PyObject* o, const Tensor& x) {
 // x, W, bias, act, residual, x_scale, w_scale, keep_pre, workspace, device_status, stream
 PyObject* linear_fwd(PyObject* const* a) {
   const Tensor& x = matrix("x", a[0], kOperands);
-  const int64_t rows = x.size(0), inner = x.size(1);
+  const int64_t rows = x.size(0);
+  const int inner = width_of("x's width", x.size(1));
   const c10::Device dev = x.device();
   const Tensor& w = weight_of(a[1], x);
-  const int64_t outer = w.size(0);
+  const int outer = width_of("W's rows", w.size(0));
   const bool e4m3 = x.scalar_type() == at::kFloat8_e4m3fn;
   if (e4m3 && (!given(a[5]) || !given(a[6]))) raise(PyExc_ValueError, "e4m3 operands need x_scale and w_scale");
   if (!e4m3 && (given(a[5]) || given(a[6]))) raise(PyExc_ValueError, "x_scale and w_scale go with e4m3 operands");
@@ -320,11 +331,11 @@ PyObject* linear_fwd(PyObject* const* a) {
   const Tensor y = empty({rows, outer}, at::kBFloat16, dev);
   Tensor pre;
   if (truth(a[7])) pre = empty({rows, outer}, at::kBFloat16, dev);
-  const Scratch ws(api.linear_fwd_workspace(rows, static_cast<int>(inner), static_cast<int>(outer), type), dev, a[8], a[9]);
+  const Scratch ws(api.linear_fwd_workspace(rows, inner, outer, type), dev, a[8], a[9]);
   check(api.linear_fwd(x.data_ptr(), ld(x), w.data_ptr(), ld(w), type, static_cast<const float*>(opt(xs)),
                        static_cast<const float*>(opt(wsc)), opt(b), b.defined() ? type_of(b.scalar_type()) : 0, opt(r),
-                       r.defined() ? ld(r) : 0, static_cast<int>(integer(a[3])), rows, static_cast<int>(inner),
-                       static_cast<int>(outer), y.data_ptr(), outer, opt(pre), outer, ws.ptr, ws.bytes, ws.status, on.stream),
+                       r.defined() ? ld(r) : 0, static_cast<int>(integer(a[3])), rows, inner,
+                       outer, y.data_ptr(), outer, opt(pre), outer, ws.ptr, ws.bytes, ws.status, on.stream),
         "uf_linear_fwd");
   on.uses(a, 11);
   Result out;
@@ -336,10 +347,11 @@ PyObject* linear_fwd(PyObject* const* a) {
 // dy, x, W, pre, act, dx, dW, dbias, workspace, device_status, stream
 PyObject* linear_bwd(PyObject* const* a) {
   const Tensor& x = matrix("x", a[1], kBf16);
-  const int64_t rows = x.size(0), inner = x.size(1);
+  const int64_t rows = x.size(0);
+  const int inner = width_of("x's width", x.size(1));
   const c10::Device dev = x.device();
   const Tensor& w = weight_of(a[2], x);
-  const int64_t outer = w.size(0);
+  const int outer = width_of("W's rows", w.size(0));
   const Tensor& dy = matrix("dy", a[0], kFloats, &dev, rows, outer);
   const int act = static_cast<int>(integer(a[4]));
   const Tensor none;
@@ -350,9 +362,9 @@ PyObject* linear_bwd(PyObject* const* a) {
   if (truth(a[5])) dx = empty({rows, inner}, at::kBFloat16, dev);
   if (truth(a[6])) dw = empty({outer, inner}, at::kBFloat16, dev);
   if (truth(a[7])) db = empty({outer}, at::kFloat, dev);
-  const Scratch ws(api.linear_bwd_workspace(rows, static_cast<int>(inner), static_cast<int>(outer)), dev, a[8], a[9]);
+  const Scratch ws(api.linear_bwd_workspace(rows, inner, outer), dev, a[8], a[9]);
   check(api.linear_bwd(dy.data_ptr(), ld(dy), type_of(dy.scalar_type()), x.data_ptr(), ld(x), w.data_ptr(), ld(w), opt(pre),
-                       act ? ld(pre) : 0, act, rows, static_cast<int>(inner), static_cast<int>(outer), opt(dx), inner,
+                       act ? ld(pre) : 0, act, rows, inner, outer, opt(dx), inner,
                        opt(dw), inner, static_cast<float*>(opt(db)), ws.ptr, ws.bytes, ws.status, on.stream),
         "uf_linear_bwd");
   on.uses(a, 11);
@@ -375,17 +387,18 @@ const Tensor& gated_weight(PyObject* o, const Tensor& x) {
 // x, W, act, keep_pre, workspace, device_status, stream
 PyObject* gated_fwd(PyObject* const* a) {
   const Tensor& x = matrix("x", a[0], kBf16);
-  const int64_t rows = x.size(0), inner = x.size(1);
+  const int64_t rows = x.size(0);
+  const int inner = width_of("x's width", x.size(1));
   const c10::Device dev = x.device();
   const Tensor& w = gated_weight(a[1], x);
-  const int64_t outer = w.size(0) / 2;
+  const int outer = width_of("W's rows", w.size(0)) / 2;
   const On on(dev, a[6]);
   const Tensor h = empty({rows, outer}, at::kBFloat16, dev);
   Tensor pre;
   if (truth(a[3])) pre = empty({rows, 2 * outer}, at::kBFloat16, dev);
-  const Scratch ws(api.gated_fwd_workspace(rows, static_cast<int>(inner), static_cast<int>(outer)), dev, a[4], a[5]);
+  const Scratch ws(api.gated_fwd_workspace(rows, inner, outer), dev, a[4], a[5]);
   check(api.gated_fwd(x.data_ptr(), ld(x), w.data_ptr(), ld(w), static_cast<int>(integer(a[2])), rows,
-                      static_cast<int>(inner), static_cast<int>(outer), h.data_ptr(), outer, opt(pre), 2 * outer, ws.ptr,
+                      inner, outer, h.data_ptr(), outer, opt(pre), 2 * outer, ws.ptr,
                       ws.bytes, ws.status, on.stream),
         "uf_gated_fwd");
   on.uses(a, 7);
@@ -398,19 +411,20 @@ PyObject* gated_fwd(PyObject* const* a) {
 // dh, x, W, pre, act, dx, dW, workspace, device_status, stream
 PyObject* gated_bwd(PyObject* const* a) {
   const Tensor& x = matrix("x", a[1], kBf16);
-  const int64_t rows = x.size(0), inner = x.size(1);
+  const int64_t rows = x.size(0);
+  const int inner = width_of("x's width", x.size(1));
   const c10::Device dev = x.device();
   const Tensor& w = gated_weight(a[2], x);
-  const int64_t outer = w.size(0) / 2;
+  const int outer = width_of("W's rows", w.size(0)) / 2;
   const Tensor& dh = matrix("dh", a[0], kBf16, &dev, rows, outer);
   const Tensor& pre = matrix("pre", a[3], kBf16, &dev, rows, 2 * outer);
   const On on(dev, a[9]);
   Tensor dx, dw;
   if (truth(a[5])) dx = empty({rows, inner}, at::kBFloat16, dev);
   if (truth(a[6])) dw = empty({2 * outer, inner}, at::kBFloat16, dev);
-  const Scratch ws(api.gated_bwd_workspace(rows, static_cast<int>(inner), static_cast<int>(outer)), dev, a[7], a[8]);
+  const Scratch ws(api.gated_bwd_workspace(rows, inner, outer), dev, a[7], a[8]);
   check(api.gated_bwd(dh.data_ptr(), ld(dh), x.data_ptr(), ld(x), w.data_ptr(), ld(w), pre.data_ptr(), ld(pre),
-                      static_cast<int>(integer(a[4])), rows, static_cast<int>(inner), static_cast<int>(outer), opt(dx),
+                      static_cast<int>(integer(a[4])), rows, inner, outer, opt(dx),
                       inner, opt(dw), inner, ws.ptr, ws.bytes, ws.status, on.stream),
         "uf_gated_bwd");
   on.uses(a, 10);

@@ -279,3 +279,24 @@ def test_inputs_of_a_call_on_another_stream_may_be_freed(L):
         torch.cuda.synchronize()
         assert all(torch.equal(got[k], want[k]) for k in want), name
         del junk
+
+
+# -------------------------------------------------------------------------------- refusals
+
+def test_widths_past_32_bits_are_refused(L):
+    """A width of 2^32 + 8 is not one of 8."""
+    wide = (1 << 32) + 8
+    rows = torch.empty(0, wide, dtype=BF, device="cuda")
+    w = torch.empty(wide, dtype=BF, device="cuda")
+    for call in (lambda: L.rmsnorm_fwd(rows, w), lambda: L.rmsnorm_bwd(rows, rows, w, torch.empty(0, device="cuda"))):
+        with pytest.raises(ValueError, match="width may be at most"):
+            call()
+    x = torch.empty(0, 8, dtype=BF, device="cuda")
+    del w
+    W = torch.empty(wide, 8, dtype=BF, device="cuda")  # 64 GiB, never written
+    with pytest.raises(ValueError, match="rows may be at most"):
+        L.linear_fwd(x, W)
+    with pytest.raises(ValueError, match="rows may be at most"):
+        L.gated_fwd(x, W)
+    del W
+    torch.cuda.empty_cache()
