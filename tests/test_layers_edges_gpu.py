@@ -1,12 +1,13 @@
 """The head's operators and the optimizer where they can go wrong beside the ordinary sizes: replaced
 storage, the ends of the formats' ranges, sides of a limit, calls from threads and other streams.
 Tolerances as in ``test_layers_gpu``."""
+import math
 import threading
 
 import pytest
 
 torch = pytest.importorskip("torch")
-from test_layers_gpu import BF, E4, F32, F64, U32, L, check, f32, rand, unpack  # noqa: F401,E402
+from test_layers_gpu import BF, E4, F32, F64, U16, U32, L, check, f32, rand, unpack  # noqa: F401,E402
 
 pytestmark = pytest.mark.gpu
 
@@ -237,6 +238,28 @@ def test_rmsnorm_e4m3_marks_a_non_finite_row(L, bad):
     assert torch.equal(got["y"].view(torch.uint8)[::2], clean["y"].view(torch.uint8)[::2])
     assert y[1].isnan().all() if bad != 1e30 else not y[1].any()
 
+
+# ---------------------------------------------------------------------------- activations
+
+@pytest.mark.parametrize("rows", [4, 40])
+def test_gelu_in_its_negative_tail(L, rows):
+    """gelu and its derivative for z from -3 down to -12, relative to their values: a rounding to bf16, and
+    2^-12 for the fp32 value (1.4e-4 of the fit, 1e-5 of the exponential's argument)."""
+    z = -torch.linspace(3, 12, rows, device="cuda").to(BF)
+    x, w = torch.zeros(rows, 64, dtype=BF, device="cuda"), torch.zeros(64, 64, dtype=BF, device="cuda")
+    x[:, 5], w[:, 5] = z, 1  # every output's argument is z itself
+    z = z.to(F64)
+    cdf = torch.special.erfc(-z / math.sqrt(2)) / 2
+    want = (z * cdf)[:, None].expand(rows, 64)
+    check("gelu", L.linear_fwd(x, w, act="gelu")["y"], want, want.abs() * (U16 * 1.01 + 2.0 ** -12))
+    want = want * z[:, None]
+    check("gated", L.gated_fwd(x, torch.cat([w, w]), act="gelu")["h"], want, want.abs() * (U16 * 1.01 + 2.0 ** -12))
+    da = cdf + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    dy, one = torch.ones(1, 64, device="cuda"), x[:1]
+    for r in range(rows):
+        pre = z[r].to(BF).expand(1, 64).contiguous()
+        got = L.linear_bwd(dy, one, w, pre=pre, act="gelu", need=("dbias",))["dbias"]
+        check("gelu'", got, da[r].expand(64), da[r].abs() * 2.0 ** -12)
 
 # ---------------------------------------------------------------------------- other streams
 
