@@ -123,7 +123,9 @@ __device__ __forceinline__ void act_grad2(float2 z, float2& a, float2& da) {
   if constexpr (ACT == kActGeluTanh) {
     const float2 s = logistic2(gelu_tanh_arg(z));
     a = mul2(z, s);
-    da = fma2(mul2(a, fma2(s, both(-1.f), both(1.f))), fma2(mul2(z, z), both(kGeluC * 0.134145f), both(kGeluC)), s);
+    // (the factor of z^2 is 0 long before z^2 overflows)
+    const float2 zz = mul2(z, z), z2 = make_float2(fminf(zz.x, 1e30f), fminf(zz.y, 1e30f));
+    da = fma2(mul2(a, fma2(s, both(-1.f), both(1.f))), fma2(z2, both(kGeluC * 0.134145f), both(kGeluC)), s);
   }
   if constexpr (ACT == kActSilu) {
     const float2 s = logistic2(mul2(z, both(-kLog2e)));

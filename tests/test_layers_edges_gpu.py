@@ -261,6 +261,26 @@ def test_gelu_in_its_negative_tail(L, rows):
         got = L.linear_bwd(dy, one, w, pre=pre, act="gelu", need=("dbias",))["dbias"]
         check("gelu'", got, da[r].expand(64), da[r].abs() * 2.0 ** -12)
 
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_activations_of_large_arguments(L, act):
+    """Far from 0 every activation is 0 or z, with a derivative of 0 or 1, up to the largest bf16."""
+    z = torch.tensor([[40.0, 1e4, 1e13, 3e19, 1e30, 3e38], [-200.0, -1e4, -1e13, -3e19, -1e30, -3e38]], device="cuda").to(BF)
+    z = torch.cat([z, z[:, :2]], 1)
+    x, w = torch.zeros(2, 64, dtype=BF, device="cuda"), torch.zeros(8, 64, dtype=BF, device="cuda")
+    x[:, 3], w[:, 3] = z[:, 0], 1
+    for c in range(8):
+        x[:, 3] = z[:, c]
+        y = L.linear_fwd(x, w, act=act)["y"]
+        assert bool((y[0] == z[0, c]).all()) and bool((y[1] == 0).all())
+    for r, want in ((0, 1.0), (1, 0.0)):
+        dy = torch.ones(1, 8, device="cuda")
+        got = L.linear_bwd(dy, x[:1], w, pre=z[r:r + 1].contiguous(), act=act, need=("dbias", "dx"))
+        assert bool((got["dbias"] == want).all()) and bool((got["dx"][:, 3] == 8 * want).all())
+        got = L.gated_bwd(dy.to(BF), x[:1], torch.cat([w, w]), torch.cat([z[r:r + 1], torch.ones_like(z[:1])], 1), act=act,
+                          need=("dx",))
+        assert got["dx"].isfinite().all()
+
 # ---------------------------------------------------------------------------- other streams
 
 def test_inputs_of_a_call_on_another_stream_may_be_freed(L):
