@@ -442,6 +442,7 @@ struct AdamTensors {
   std::vector<float*> ms, vs;
   std::vector<const void*> g;
   std::vector<int64_t> sizes;
+  std::vector<c10::TensorImpl*> written;  // of the lists, which hold them
   c10::Device dev{c10::kCPU};
   at::ScalarType ptype = at::kFloat, stype = at::kFloat, gtype = at::kFloat;
 };
@@ -493,12 +494,15 @@ AdamTensors adam_tensors(PyObject* const* a) {
   auto keep = [&](auto& to) {
     to.reserve(static_cast<size_t>(n));
     return [&](int64_t, const Tensor& t) {
+      q.written.push_back(t.unsafeGetTensorImpl());
       to.push_back(static_cast<typename std::decay_t<decltype(to)>::value_type>(t.data_ptr()));
     };
   };
   q.p.reserve(static_cast<size_t>(n));
   q.sizes.reserve(static_cast<size_t>(n));
+  q.written.reserve(static_cast<size_t>(n) * 6);
   each(q.dev, "params", a[0], kFloats, n, nullptr, &q.ptype, [&](int64_t, const Tensor& t) {
+    q.written.push_back(t.unsafeGetTensorImpl());
     q.p.push_back(t.data_ptr());
     q.sizes.push_back(t.numel());
   });
@@ -533,8 +537,16 @@ PyObject* adamw_check(PyObject* const* a) {
 // params, m, v, m_scale, v_scale, copies, grads, lr (float or tensor), betas[0], betas[1], eps, weight_decay,
 // step, step_dev, seed, grad_scale, stream
 PyObject* adamw_step(PyObject* const* a) {
-  AdamTensors q = adam_tensors(a);
+  PyObject* const* lists = a;
   a += 6;
+  // (numbers first: none of them may run code once addresses are taken)
+  const bool lr_tensor = THPVariable_Check(a[1]);
+  const float lr = lr_tensor ? 0.f : static_cast<float>(number(a[1]));
+  const double beta1 = number(a[2]), beta2 = number(a[3]);
+  const float eps = static_cast<float>(number(a[4])), decay = static_cast<float>(number(a[5]));
+  const int64_t step = integer(a[6]);
+  const uint32_t seed = static_cast<uint32_t>(integer(a[8]));
+  AdamTensors q = adam_tensors(lists);
   const int64_t n = static_cast<int64_t>(q.sizes.size());
   q.g.reserve(static_cast<size_t>(n));
   each(q.dev, "grads", a[0], kFloats, n, &q.sizes, &q.gtype, [&](int64_t, const Tensor& t) { q.g.push_back(t.data_ptr()); });
@@ -547,20 +559,19 @@ PyObject* adamw_step(PyObject* const* a) {
             q.dev.str().c_str());
     return THPVariable_Unpack(o).data_ptr();
   };
-  const bool lr_tensor = THPVariable_Check(a[1]);
   const auto* lr_dev = static_cast<const float*>(lr_tensor ? scalar("lr", a[1], at::kFloat) : nullptr);
-  const float lr = lr_tensor ? 0.f : static_cast<float>(number(a[1]));
   const auto* step_dev = static_cast<const int64_t*>(scalar("step_dev", a[7], at::kLong));
   const auto* gs = static_cast<const float*>(scalar("grad_scale", a[9], at::kFloat));
   const On on(q.dev, a[10]);
   check(api.adamw_step(static_cast<int>(n), q.p.data(), q.g.data(), q.m.data(), q.v.data(),
                        q.ms.empty() ? nullptr : q.ms.data(), q.vs.empty() ? nullptr : q.vs.data(),
                        q.copy.empty() ? nullptr : q.copy.data(), q.sizes.data(), type_of(q.ptype), type_of(q.gtype),
-                       type_of(q.stype), lr, lr_dev, number(a[2]), number(a[3]),
-                       static_cast<float>(number(a[4])), static_cast<float>(number(a[5])), integer(a[6]), step_dev,
-                       static_cast<uint32_t>(integer(a[8])), gs, on.stream),
+                       type_of(q.stype), lr, lr_dev, beta1, beta2, eps, decay, step, step_dev, seed, gs, on.stream),
         "uf_adamw_step");
-  on.uses(a - 6, 17);
+  on.uses(lists, 17);
+  // as torch's in-place operations do: a backward that saved one of them raises
+  for (c10::TensorImpl* t : q.written)
+    if (!t->is_inference()) t->bump_version();
   Py_RETURN_NONE;
 }
 

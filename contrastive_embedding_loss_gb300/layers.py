@@ -14,6 +14,9 @@ A call on another ``stream`` than the current one does not wait for the current 
 orders the streams, as for any torch work on another stream.  Inputs may be freed right after the
 call; its outputs belong to ``stream`` (``Tensor.record_stream`` before they are freed while a
 third stream uses them).
+
+Nothing here is recorded by autograd: outputs have no gradient function, whatever the inputs
+require; the backward functions are called by the program.
 """
 from __future__ import annotations
 

@@ -172,6 +172,25 @@ def test_adamw_8bit_momentum_dies_out(L):
     assert not opt.m[0].to(F32).any() and not opt.m_scale[0].any()
 
 
+def test_adamw_counts_its_writes_for_autograd(L):
+    """A backward that saved a parameter raises after a step, as with any write in place; an inference
+    tensor has no count."""
+    p, g = [rand(1, 100).requires_grad_()], [rand(2, 100)]
+    opt = L.AdamW(p, *L.AdamW.new_states(p, 8), copies=[p[0].detach().bfloat16()])
+    written = [p[0], opt.m[0], opt.v[0], opt.m_scale[0], opt.v_scale[0], opt.copies[0]]
+    versions = [t._version for t in written]
+    loss = (p[0] * p[0]).sum()
+    opt.step(g, lr=1e-2)
+    assert all(t._version > v for t, v in zip(written, versions)) and g[0]._version == 0
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        p = [rand(1, 100)]
+        start = p[0].clone()
+        L.AdamW(p, *L.AdamW.new_states(p)).step(g, lr=1e-2)
+        assert not torch.equal(p[0], start)
+
+
 # ------------------------------------------------------------------------------- RMS norm
 
 def test_rmsnorm_backward_from_two_threads(L):
