@@ -7,7 +7,8 @@ import threading
 import pytest
 
 torch = pytest.importorskip("torch")
-from test_layers_gpu import BF, E4, F32, F64, U16, U32, L, check, f32, rand, unpack  # noqa: F401,E402
+from test_layers_gpu import (BF, E4, F32, F64, FAST, U16, U32, L, act64, adam64, check, f32, inside, norm_bwd64,  # noqa: F401,E402
+                             rand, unpack)
 
 pytestmark = pytest.mark.gpu
 
@@ -191,6 +192,39 @@ def test_adamw_counts_its_writes_for_autograd(L):
         assert not torch.equal(p[0], start)
 
 
+@pytest.mark.parametrize("gt", [F32, BF])
+@pytest.mark.parametrize("n,off", [(1000, 0), (1000, 3), (66000, 0)])
+def test_adamw_8bit_states_of_bf16_parameters(L, n, off, gt):
+    """Parameters and codes are neighbours of the values that they stand for."""
+    p, g = rand(1, n + off, dtype=BF)[off:], rand(2, n, scale=1e-2, dtype=gt)
+    blocks = -(-n // 256)
+    q = [(rand(3 + i, n + off).abs() * 100).clamp(0, 448).to(E4)[off:] for i in range(2)]
+    s = [rand(5 + i, blocks).abs() * 1e-4 for i in range(2)]
+    m0, r0 = unpack(q[0], s[0]), unpack(q[1], s[1])
+    b1, b2, lr, t = 0.9, 0.999, f32(1e-3), 10
+    wp, wm, wv = adam64(p, g, m0, r0 * r0, t, lr, b1, b2, f32(1e-8), f32(0.01))
+    L.AdamW([p], [q[0]], [q[1]], [s[0]], [s[1]], step=t - 1).step([g], lr=1e-3, seed=77)
+    step = lr * (wm.abs() + g.to(F64).abs()) / (1 - b1 ** t) / ((wv / (1 - b2 ** t)).sqrt() + 1e-8)
+    # less than one unit away: 2^-7 of the value (16 random bits: a unit's last 2^-16 never rounds up)
+    check("p", p, wp, wp.abs() * 2.0 ** -7 * 1.0001 + step * 32 * U32 + 1e-30)
+    for name, want, code, scale in (("m", wm, q[0], s[0]), ("v", wv.sqrt(), q[1], s[1])):
+        top = torch.nn.functional.pad(want.abs(), (0, blocks * 256 - n)).reshape(blocks, 256).amax(1)
+        check(name + " scale", scale, top / 448, top / 448 * 16 * U32 + 1e-40)
+        unit = scale.to(F64).repeat_interleave(256)[:n]
+        check(name, unpack(code, scale), want, torch.maximum(want.abs() * 2.0 ** -3, unit * 2.0 ** -9) * 1.0001)
+
+
+def test_adamw_bf16_parameters_and_gradients_in_fp32_states(L):
+    p, g = rand(1, 4099, dtype=BF), rand(2, 4099, scale=1e-2, dtype=BF)
+    m, v = rand(3, 4099, scale=1e-3), rand(4, 4099, scale=1e-2).square()
+    wp, wm, wv = adam64(p, g, m, v, 5, f32(1e-3), eps=f32(1e-8), wd=f32(0.01))
+    L.AdamW([p], [m], [v], step=4).step([g], lr=1e-3)
+    check("m", m, wm, (wm.abs() + g.to(F64).abs()) * 4 * U32 + 1e-30)
+    check("v", v, wv, wv * 6 * U32 + 1e-38)
+    slack = 1e-3 * (g.to(F64).abs() + wm.abs()) / (1 - 0.9 ** 5) / ((wv / (1 - 0.999 ** 5)).sqrt() + 1e-8)
+    check("p", p, wp, wp.abs() * 2.0 ** -7 * 1.0001 + slack * 32 * U32 + 1e-30)
+
+
 # ------------------------------------------------------------------------------- RMS norm
 
 def test_rmsnorm_backward_from_two_threads(L):
@@ -256,6 +290,155 @@ def test_rmsnorm_e4m3_marks_a_non_finite_row(L, bad):
     y = got["y"].to(F32) * got["scale"][:, None]
     assert torch.equal(got["y"].view(torch.uint8)[::2], clean["y"].view(torch.uint8)[::2])
     assert y[1].isnan().all() if bad != 1e30 else not y[1].any()
+
+
+def norm_bwd_check(L, dy, s, w, ds):
+    rows, width = s.shape
+    rho = (s.to(F64).square().mean(1) + 1e-6).rsqrt().to(F32)
+    got = L.rmsnorm_bwd(dy, s, w, rho, d_stream=ds)
+    dx, size, dw, dw_size = norm_bwd64(dy.to(F64), s.to(F64), w.to(F64), rho.to(F64), None if ds is None else ds.to(F64))
+    check("dx", got["dx"], dx, size * (width + 16) * U32 + (dx.abs() * U16 if s.dtype == BF else 0) + 1e-30)
+    check("dweight", got["dweight"], dw, dw_size * (rows + 16) * U32 + 1e-30)
+
+
+# For each number of threads a row: odd widths, whose rows start at every alignment, and rows enough
+# that a block takes several, 8 or a multiple apart.
+MANY_ROWS = [(3001, 77), (3003, 515), (3001, 1023), (5003, 1031), (1300, 2051), (1300, 4099), (700, 8191), (700, 16383)]
+
+
+@pytest.mark.parametrize("rows,width", MANY_ROWS)
+@pytest.mark.parametrize("dyt,st,carry", [(BF, BF, True), (F32, F32, False), (BF, F32, True), (F32, BF, False)])
+def test_rmsnorm_bwd_of_many_rows_of_odd_width(L, rows, width, dyt, st, carry):
+    dy, s = rand(2, rows, width, dtype=dyt), rand(1, rows, width, dtype=st)
+    norm_bwd_check(L, dy, s, 1 + rand(3, width, scale=0.1), rand(4, rows, width, dtype=st) if carry else None)
+
+
+@pytest.mark.parametrize("rows,width", [(3001, 500), (700, 4100)])
+@pytest.mark.parametrize("st", [BF, F32])
+def test_rmsnorm_bwd_of_rows_with_an_odd_pitch(L, rows, width, st):
+    """All arrays in step with one another, in rows of width + 5 elements: so is the returned dx's
+    misalignment to theirs, and the accesses are single elements unless dx has the same pitch."""
+    dy, s, ds = (rand(i, rows, width + 5, dtype=t)[:, :width] for i, t in ((1, BF), (2, st), (3, st)))
+    norm_bwd_check(L, dy, s, 1 + rand(4, width, scale=0.1), ds)
+    # through the C ABI into a dx of that pitch: vectors from a row's first boundary on
+    lib, pitch = L._load(), width + 5
+    rho = (s.to(F64).square().mean(1) + 1e-6).rsqrt().to(F32)
+    w, dw = 1 + rand(4, width, scale=0.1), torch.empty(width, device="cuda")
+    dx = torch.full((rows, pitch), 7.0, device="cuda").to(st)
+    ws = torch.empty(lib.uf_rmsnorm_bwd_workspace(rows, width), dtype=torch.uint8, device="cuda")
+    kind = 0 if st == BF else 1
+    assert 0 == lib.uf_rmsnorm_bwd(dy.data_ptr(), pitch, 0, s.data_ptr(), pitch, kind, w.data_ptr(), 1, rho.data_ptr(),
+                                   ds.data_ptr(), pitch, rows, width, dx.data_ptr(), pitch, dw.data_ptr(), ws.data_ptr(),
+                                   ws.numel(), torch.cuda.current_stream().cuda_stream)
+    want, size, dw64, dw_size = norm_bwd64(dy.to(F64), s.to(F64), w.to(F64), rho.to(F64), ds.to(F64))
+    check("dx", dx[:, :width], want, size * (width + 16) * U32 + (want.abs() * U16 if st == BF else 0) + 1e-30)
+    check("dweight", dw, dw64, dw_size * (rows + 16) * U32 + 1e-30)
+    assert bool((dx[:, width:] == 7.0).all())
+
+
+@pytest.mark.parametrize("rows,width", [(1300, 600), (700, 1500), (700, 5000), (400, 9000)])
+@pytest.mark.parametrize("st", [BF, F32])
+def test_rmsnorm_out_of_step(L, rows, width, st):
+    """Arrays whose 16-byte boundaries lie at different elements: single elements, 32 to 512 threads a row."""
+    x, r = inside(rand(1, rows, width, dtype=BF), pad_cols=3), rand(2, rows, width, scale=2.0, dtype=st)
+    w = 1 + rand(3, width, scale=0.1, dtype=BF)
+    for out in ("bf16", "e4m3"):
+        got = L.rmsnorm_fwd(x, w, residual=r, out=out)
+        s = x.to(F64) + r.to(F64)
+        y = s * (s.square().mean(1, keepdim=True) + 1e-6).rsqrt() * w.to(F64)
+        rel = (width / 2 + 24) * U32
+        check("stream", got["stream"], s, s.abs() * (U16 * 1.01 if st == BF else 2 * U32) + 1e-30)
+        if out == "bf16":
+            check("y", got["y"], y, y.abs() * (U16 + 2 * rel) + 1e-30)
+        else:
+            scale = got["scale"].to(F64)[:, None]
+            check("y", got["y"].to(F64) * scale, y, torch.maximum(y.abs() * 2.0 ** -4, scale * 2.0 ** -10) * 1.001 + y.abs() * rel)
+    norm_bwd_check(L, inside(rand(4, rows, width, dtype=BF), pad_cols=3), r, w, rand(5, rows, width, dtype=st))
+
+
+@pytest.mark.parametrize("width", [1000, 1001])
+def test_rmsnorm_bwd_of_a_bf16_weight(L, width):
+    norm_bwd_check(L, rand(1, 300, width, dtype=BF), rand(2, 300, width), 1 + rand(3, width, scale=0.1, dtype=BF), None)
+
+
+# -------------------------------------------------------------------------------- products
+
+@pytest.mark.parametrize("rows", [5, 300, 3000])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_linear_bwd_of_what_is_asked(L, rows, act):
+    inner, outer = 264, 520
+    x, w, dy = rand(1, rows, inner, dtype=BF), rand(2, outer, inner, dtype=BF), rand(3, rows, outer, dtype=BF)
+    pre = rand(4, rows, outer, dtype=BF) if act != "none" else None
+    da = 1.0 if pre is None else act64(pre.to(F64), act)[1]
+    dz = dy.to(F64) * da
+    off = torch.zeros_like(dz) if pre is None else dy.to(F64).abs() * 4 * FAST
+    rounded = off + (0 if pre is None else dz.abs() * U16)
+    X, W = x.to(F64), w.to(F64)
+    want = {"dx": dz @ W, "dW": dz.t() @ X, "dbias": dz.sum(0)}
+    bound = {"dx": rounded @ W.abs() * 1.01 + dz.abs() @ W.abs() * (outer + 8) * 2 * U32 + want["dx"].abs() * U16 * 1.01 + 1e-30,
+             "dW": rounded.t() @ X.abs() * 1.01 + dz.abs().t() @ X.abs() * (rows + 8) * 2 * U32 + want["dW"].abs() * U16 * 1.01 + 1e-30,
+             "dbias": off.sum(0) + dz.abs().sum(0) * (rows + 8) * U32 + 1e-30}
+    for need in (("dx",), ("dW",), ("dbias",), ("dx", "dbias"), ("dW", "dbias"), ("dx", "dW"), ()):
+        got = L.linear_bwd(dy, x, w, pre=pre, act=act, need=need)
+        assert set(got) == set(need)
+        for k in need:
+            check(f"{k} of {need}", got[k], want[k], bound[k])
+    with pytest.raises(ValueError, match="need names"):
+        L.linear_bwd(dy, x, w, need=("dy",))
+
+
+@pytest.mark.parametrize("rows", [5, 300, 3000])
+def test_gated_bwd_of_what_is_asked(L, rows):
+    inner, outer = 264, 136
+    x, w, dh = rand(1, rows, inner, dtype=BF), rand(2, 2 * outer, inner, dtype=BF), rand(3, rows, outer, dtype=BF)
+    pre = rand(4, rows, 2 * outer, dtype=BF)
+    g, u = pre.to(F64).split(outer, 1)
+    a, da = act64(g, "silu")
+    d = torch.cat([dh.to(F64) * u * da, dh.to(F64) * a], 1)
+    err = torch.cat([(dh.to(F64) * u).abs() * 4 * FAST, (dh.to(F64) * g).abs() * FAST], 1) + d.abs() * U16 * 1.01
+    X, W = x.to(F64), w.to(F64)
+    want = {"dx": d @ W, "dW": d.t() @ X}
+    bound = {"dx": err @ W.abs() + d.abs() @ W.abs() * (2 * outer + 8) * 2 * U32 + want["dx"].abs() * U16 * 1.01 + 1e-30,
+             "dW": err.t() @ X.abs() + d.abs().t() @ X.abs() * (rows + 8) * 2 * U32 + want["dW"].abs() * U16 * 1.01 + 1e-30}
+    for need in (("dx",), ("dW",), ("dx", "dW"), ()):
+        got = L.gated_bwd(dh, x, w, pre, need=need)
+        assert set(got) == set(need)
+        for k in need:
+            check(f"{k} of {need}", got[k], want[k], bound[k])
+
+
+def test_the_callers_workspace_and_status(L):
+    from contrastive_embedding_loss_gb300.binding import UfError
+
+    lib = L._load()
+    x, w, dy = rand(1, 64, 8192, dtype=BF), rand(2, 256, 8192, dtype=BF), rand(3, 64, 256, dtype=BF)
+    pre, rstd, n = rand(4, 64, 256, dtype=BF), torch.ones(64, device="cuda"), torch.ones(256, device="cuda")
+    calls = {  # (call, its scratch, whether it takes a status word)
+        "rmsnorm_bwd": (lambda **k: L.rmsnorm_bwd(dy, pre, n, rstd, **k), lib.uf_rmsnorm_bwd_workspace(64, 256), False),
+        "linear_fwd": (lambda **k: L.linear_fwd(x, w, **k), lib.uf_linear_fwd_workspace(64, 8192, 256, 0), True),
+        "linear_bwd": (lambda **k: L.linear_bwd(dy, x, w, pre=pre, act="silu", **k), lib.uf_linear_bwd_workspace(64, 8192, 256), True),
+        "gated_fwd": (lambda **k: L.gated_fwd(x, w, **k), lib.uf_gated_fwd_workspace(64, 8192, 128), True),
+        "gated_bwd": (lambda **k: L.gated_bwd(dy[:, :128], x, w, pre, **k), lib.uf_gated_bwd_workspace(64, 8192, 128), True),
+    }
+    for name, (call, need, takes_status) in calls.items():
+        assert need > 0, name
+        want = call()
+        ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = call(workspace=ws[:need], **({"device_status": status} if takes_status else {}))
+        assert all(torch.equal(got[k], want[k]) for k in want), name
+        assert int(status) == 0 and bool((ws[need:] == 255).all()), name
+        with pytest.raises(UfError, match="workspace-too-small"):
+            call(workspace=ws[:need - 1])
+        with pytest.raises(UfError, match="invalid-argument"):
+            call(workspace=ws[16:])  # not on 256 bytes
+        for bad in (ws.float(), ws[::2], ws.cpu(), need):
+            with pytest.raises(TypeError, match="workspace"):
+                call(workspace=bad)
+        if takes_status:
+            for bad in (status.float(), status.cpu(), status[:0], 0):
+                with pytest.raises(TypeError, match="device_status"):
+                    call(device_status=bad)
 
 
 # ---------------------------------------------------------------------------- activations
