@@ -5,8 +5,13 @@
 // once, 16 bytes a thread and access.  A block of act_bwd owns up to 256 columns (8 a thread) and
 // a range of rows (8 or more at a time); its column sums stay in registers, are joined across the
 // row lanes in shared memory and written as one row of partial sums, which the column-sum kernel
-// adds in a fixed order.  16384 x 4096 with gelu: 64 us (403 MB, 6.3 TB/s); the gated block's pass
-// over 16384 x 2816: 63 us (461 MB).
+// adds in a fixed order.  16384 x 4096 with gelu: 66 us (403 MB, 6.1 TB/s); the gated block's pass
+// over 16384 x 2816: 64 us (461 MB).
+//
+// dz and [dg | du] are rounded to bf16, an fp32 dy's too, because the products that read them take
+// bf16 operands: in fp32 they would go by tf32 at half the rate, or as two bf16 terms at a third of it.
+// It puts the gradients 2.3e-3 of their norm from the exact ones, where the rounding of the outputs
+// alone makes 1.7e-3.  The bias gradient sums the unrounded values.
 #include <algorithm>
 #include "layers.cuh"
 

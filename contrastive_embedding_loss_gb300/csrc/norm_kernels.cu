@@ -9,7 +9,7 @@
 // every array crosses HBM once: TPR threads share a row, 16 or 32 values each at most (TPR = 32 to
 // 1024 by the width).  The backward's blocks walk rows with a stride and keep their columns'
 // part of dw in registers; the blocks' parts are summed by a second small kernel in a fixed order.
-// 16384 x 4096 with a bf16 residual to e4m3: 67 us (470 MB, 7.0 TB/s); the backward of 65536 x 1024
+// 16384 x 4096 with a bf16 residual to e4m3: 68 us (470 MB, 6.9 TB/s); the backward of 65536 x 1024
 // with an fp32 stream: 139 us (940 MB, 6.7 TB/s).
 //
 // Rows of any width and alignment: a row is cut into a head of up to 7 elements that ends at a

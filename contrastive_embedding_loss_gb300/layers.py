@@ -8,7 +8,8 @@ C call on the current stream (or ``stream``, a ``torch.cuda.Stream``); what is w
 
 The functions return dicts, as ``binding.contrastive_fwd_bwd`` does.  Matrices are 2-D CUDA
 tensors whose rows may be strided (a stride of 1 within a row).  ``workspace`` may be a
-preallocated uint8 CUDA tensor of at least the C entry point's workspace size.
+preallocated uint8 CUDA tensor of at least the C entry point's workspace size, ``device_status`` an
+int32 one that a kernel sets to ``binding.UF_DEVICE_TIMEOUT`` if a bounded wait in it ran out.
 
 A call on another ``stream`` than the current one does not wait for the current one: the caller
 orders the streams, as for any torch work on another stream.  Inputs may be freed right after the

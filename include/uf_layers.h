@@ -152,7 +152,8 @@ UF_API uf_status_t uf_gated_bwd(const void* dh, int64_t lddh, const void* x, int
  *   seed         of the stochastic rounding (with step_dev the count is added to it): give every
  *                step its own.  Element i of tensor k draws h = H(i + H(seed + 0x9E3779B9 k)), all
  *                mod 2^32, H the two-multiplication integer hash (x ^= x >> 16; x *= 0x7feb352d;
- *                x ^= x >> 15; x *= 0x846ca68b; x ^= x >> 16); m takes its low 16 bits, v its high
+ *                x ^= x >> 15; x *= 0x846ca68b; x ^= x >> 16; from C. Wellons, Prospecting for Hash
+ *                Functions, 2018); m takes its low 16 bits, v its high
  *                ones, a bf16 parameter the low 16 of H(h ^ 0x9E3779B9).
  *   grad_scale_dev  device fp32 scalar (a clipping or unscaling factor), or NULL for 1.
  */
