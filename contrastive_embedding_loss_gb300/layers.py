@@ -91,6 +91,11 @@ def _act(act):
     return ACTS[act]
 
 
+def _sequence(tensors):
+    """A list or tuple as it is, other iterables (a generator, read once) as a list."""
+    return tensors if tensors is None or isinstance(tensors, (list, tuple)) else list(tensors)
+
+
 def _asked(need, names):
     if any(k not in names for k in need):
         raise ValueError(f"need names {', '.join(names[:-1])} or {names[-1]}")
@@ -167,9 +172,10 @@ class AdamW:
 
     def __init__(self, params, m, v, m_scale=None, v_scale=None, copies=None, betas=(0.9, 0.999), eps=1e-8,
                  weight_decay=0.01, step=0):
-        self.params, self.m, self.v, self.m_scale, self.v_scale, self.copies = params, m, v, m_scale, v_scale, copies
+        lists = tuple(_sequence(t) for t in (params, m, v, m_scale, v_scale, copies))
+        self.params, self.m, self.v, self.m_scale, self.v_scale, self.copies = lists
         self.betas, self.eps, self.weight_decay, self.t = betas, eps, weight_decay, step
-        _native.adamw_check(params, m, v, m_scale, v_scale, copies)
+        _native.adamw_check(*lists)
 
     @staticmethod
     def new_states(params, bits=32):
@@ -192,6 +198,6 @@ class AdamW:
         t = self.t + 1
         if seed is None:
             seed = 0 if step_dev is not None else t
-        _native.adamw_step(self.params, self.m, self.v, self.m_scale, self.v_scale, self.copies, grads, lr, *self.betas,
-                           self.eps, self.weight_decay, t, step_dev, seed & 0xFFFFFFFF, grad_scale, stream)
+        _native.adamw_step(self.params, self.m, self.v, self.m_scale, self.v_scale, self.copies, _sequence(grads), lr,
+                           *self.betas, self.eps, self.weight_decay, t, step_dev, seed & 0xFFFFFFFF, grad_scale, stream)
         self.t = t

@@ -55,6 +55,18 @@ def test_adamw_follows_replaced_entries_of_its_lists(L):
     assert torch.equal(opt.params[0], new) and torch.equal(opt.m[0], m) and torch.equal(opt.v[0], v)
 
 
+def test_adamw_takes_any_iterable(L):
+    want, g = [rand(1, 500), rand(2, 300)], [rand(3, 500), rand(4, 300)]
+    params = [t.clone() for t in want]
+    opt = L.AdamW(want, *L.AdamW.new_states(want, 8), copies=[t.bfloat16() for t in want])
+    other = L.AdamW((t for t in params), *(iter(ts) for ts in L.AdamW.new_states(params, 8)),
+                    copies=(t.bfloat16() for t in params))
+    for _ in range(2):
+        opt.step(g, lr=1e-2)
+        other.step((t for t in g), lr=1e-2)
+    assert all(torch.equal(a, b) for a, b in zip(want, params))
+
+
 def test_adamw_refuses_tensors_that_no_longer_fit(L):
     p, g = [rand(1, 500)], [rand(2, 500)]
     opt = L.AdamW(p, *L.AdamW.new_states(p))
