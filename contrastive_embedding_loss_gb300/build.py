@@ -3,7 +3,7 @@
 nvcc compiles each translation unit for sm_103a only (in parallel), then links one
 shared object with the CUDA runtime linked statically, so loading the library needs no
 GPU and no libcuda (the driver entry point is resolved at the first call).  The library needs
-nvcc alone.  Where torch is installed, g++ builds ``_layers_native-<torch's version>.so`` beside
+nvcc alone.  Where torch for CUDA is installed, g++ builds ``_layers_native-<torch's version>.so`` beside
 it, the Python module that calls the library with torch tensors: one that was built against
 another torch is not found, rather than loaded.
 """
@@ -79,7 +79,7 @@ def native_path() -> str:
 
 def _build_native(force: bool) -> None:
     spec = importlib.util.find_spec("torch")
-    if spec is None:
+    if spec is None or not os.path.exists(os.path.join(os.path.dirname(spec.origin), "lib", "libc10_cuda.so")):
         return
     out = native_path()
     digest = _digest(torch_version())

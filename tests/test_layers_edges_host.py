@@ -1,5 +1,6 @@
 """Host-side edges of the head's operators (no GPU needed)."""
 import ctypes
+import importlib.machinery
 import importlib.metadata
 import os
 import random
@@ -87,6 +88,14 @@ def test_the_library_builds_without_torch(compilers):
     out = build.build()
     assert os.path.exists(out) and not os.path.exists(build.native_path())
     assert calls == ["nvcc"] * (len(build.SOURCES) + 1)
+
+
+def test_the_library_builds_beside_a_torch_without_cuda(compilers, tmp_path):
+    build, calls, monkeypatch = compilers
+    spec = importlib.machinery.ModuleSpec("torch", None, origin=str(tmp_path / "torch" / "__init__.py"))
+    monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: spec)
+    out = build.build()
+    assert os.path.exists(out) and not os.path.exists(build.native_path()) and "g++" not in calls
 
 
 def test_another_torch_rebuilds_the_binding_alone(compilers):
